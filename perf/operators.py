@@ -254,8 +254,7 @@ def _own_logp(s, dobb):
     if case["top"]:
         o["top_ids"], o["top_logp"] = r.top_ids, r.top_logp
     if case["grad"]:
-        o["dlogits"] = dobb.log_probs_backward(s["logits"], s["targets"], r.lse, s["g"], entropy=r.entropy, grad_entropy=s["h"],
-                                               scale=case["scale"])
+        o["dlogits"] = dobb.log_probs_backward(s["logits"], s["targets"], r, s["g"], grad_entropy=s["h"])
     return o
 
 
