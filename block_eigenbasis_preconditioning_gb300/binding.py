@@ -29,6 +29,7 @@ FLAG_NONFINITE_X = 1
 FLAG_NONFINITE_G = 2
 FLAG_NONFINITE_A = 4
 FLAG_NOT_CONVERGED = 8
+FLAG_BAD_TOKEN = 16
 
 # (name, restype, argtypes) of every exported symbol
 _c = ctypes
@@ -77,6 +78,21 @@ SIGNATURES = [
     ("dobb_eigh_noalloc", _c.c_int, [_VP, _VP, _VP, _c.c_int, _c.c_int, _c.c_int,
                                      _c.POINTER(_c.c_uint32), _VP]),
     ("dobb_eigh_noalloc_last_error", _c.c_char_p, []),
+    ("dobb_log_probs", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int,
+                                  _c.c_float, _c.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    ("dobb_log_probs_backward", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP,
+                                           _c.c_int, _c.c_float, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                           _c.c_int64, _VP]),
+    ("dobb_embedding", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int,
+                                  _c.c_int64, _c.c_float, _VP, _c.c_int, _c.c_int64, _VP, _VP]),
+    ("dobb_embedding_backward_bytes", _c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64]),
+    ("dobb_embedding_backward", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP,
+                                           _c.c_int, _c.c_int64, _c.c_float, _VP, _c.c_int,
+                                           _c.c_int64, _c.c_int, _VP, _VP, _c.c_size_t, _VP]),
+    ("dobb_clip_grads_bytes", _c.c_size_t, [_c.c_int, _I64P]),
+    ("dobb_clip_grads", _c.c_int, [_c.c_int, _c.POINTER(_VP), _c.POINTER(_c.c_int32), _I64P,
+                                   _c.c_float, _c.POINTER(_VP), _c.POINTER(_c.c_int32), _VP, _VP,
+                                   _VP, _c.c_size_t, _VP]),
 ]
 
 

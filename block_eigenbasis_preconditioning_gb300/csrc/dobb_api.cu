@@ -23,18 +23,24 @@
 using namespace dobb;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
 
-dobb_status fail(dobb_status st, const char* fmt, ...) {
+dobb_status dobb::fail(dobb_status st, const char* fmt, ...) noexcept {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  g_err = buf;
+  try {
+    g_err = buf;
+  } catch (...) {  // no memory for the message: the status still says what failed
+    g_err.clear();
+  }
   return st;
 }
+
+namespace {
 
 #define CUDA_TRY(expr)                                                                   \
   do {                                                                                   \

@@ -12,6 +12,9 @@
 
 namespace dobb {
 
+// Records the message of dobb_last_error() and returns `st`.
+dobb_status fail(dobb_status st, const char* fmt, ...) noexcept;
+
 // Matrices addressed by one grouped launch; larger sets are split into
 // several launches of at most this many matrices (pointer tables travel in
 // the kernel parameter block).

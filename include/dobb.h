@@ -338,6 +338,135 @@ dobb_status dobb_eigh_noalloc(const float* A_dev, float* Q_dev, float* lam_dev, 
                               int max_sweeps, uint32_t* flags_host, void* stream);
 const char* dobb_eigh_noalloc_last_error(void);
 
+/* ------------------------------------------------------------------------
+ * The two ends of a language model, and its gradients before a step.
+ *
+ * The pages have no counterpart of these calls.  They make and prepare what
+ * dobb_step consumes for the token embedding and the output head: the log
+ * probabilities of given tokens and their gradient with respect to the
+ * logits, the embedding lookup and its gradient, and the clipping of all
+ * gradients by their global norm (written in the parameter dtype that
+ * dobb_step reads).  They take no handle: every call works on the current
+ * device, is asynchronous on `stream`, allocates nothing, synchronises
+ * nothing and keeps nothing for the next call.  Rows and tensors may start at
+ * any multiple of their element size.  Sums, maxima, norms and softmax
+ * statistics are held in 32 bits or more; a result of fewer bits is rounded
+ * once (nearest, ties to even).  Results do not depend on the order in which
+ * the GPU runs the work: the same call on the same data gives the same bits.
+ * Token indices are int32 or int64 (token_bytes 4 or 8).  `flags_dev` is an
+ * optional device uint32 that condition bits are OR-ed into. */
+#define DOBB_FLAG_BAD_TOKEN 16u /* a token index >= vocab                       */
+
+/* Largest number of alternatives dobb_log_probs returns per row. */
+#define DOBB_MAX_TOP_K 32
+
+/* Log probabilities of given tokens, entropies and the most likely
+ * alternatives.  With y_j = scale * logits[r][j], j < vocab:
+ *   row_max[r] = max_j logits[r][j]
+ *   log_sum[r] = log sum_j exp(scale * (logits[r][j] - row_max[r]))
+ *   lse[r]     = scale * row_max[r] + log_sum[r]
+ *   logp[r]    = y_t - lse[r],  t = tokens[r]
+ *   entropy[r] = - sum_j p_j log p_j,  p_j = exp(y_j - lse[r])
+ *   top_ids[r][0 .. top_k): the indices of the top_k largest logits, largest
+ *     first, ties by the lowest index (-0 equals 0, a NaN counts as larger
+ *     than every number); top_logp: their log probabilities.
+ * -inf logits are tokens that cannot occur.  A row of -inf alone has row_max
+ * = log_sum = lse = -inf, logp -inf and entropy 0, its alternatives are
+ * 0, 1, ... with -inf.  A row with a NaN or +inf logit has NaN for log_sum,
+ * lse, logp, entropy and top_logp.  A token < 0 stands for none: logp 0.  A
+ * token >= vocab has logp NaN and sets DOBB_FLAG_BAD_TOKEN.
+ *   logits_dev  rows x vocab, row r at r * row_stride elements
+ *   scale       > 0 and finite (the inverse temperature)
+ *   top_k       0 ... min(DOBB_MAX_TOP_K, vocab)
+ *   logp, lse, row_max, log_sum, entropy  rows floats each; entropy and lse
+ *               may be NULL (not computed)
+ *   top_ids, top_logp  rows x top_k, NULL when top_k is 0
+ * rows may be 0 (nothing is done); vocab is 1 ... 2^31 - 1. */
+dobb_status dobb_log_probs(const void* logits_dev, dobb_dtype logits_dtype, int64_t rows,
+                           int64_t vocab, int64_t row_stride, const void* tokens_dev,
+                           int token_bytes, float scale, int top_k, float* logp_dev,
+                           float* lse_dev, float* row_max_dev, float* log_sum_dev,
+                           float* entropy_dev, int32_t* top_ids_dev, float* top_logp_dev,
+                           uint32_t* flags_dev, void* stream);
+
+/* Gradient of dobb_log_probs with respect to the logits, for the gradients g
+ * of logp, h of entropy and l of lse (rows floats each; h and l may be NULL,
+ * h needs entropy_dev):
+ *   dlogits[r][j] = scale * (g (1[j = t] - p_j) + l p_j
+ *                            - h p_j (log p_j + entropy[r]))
+ * with p_j log p_j = 0 where p_j = 0.  A row of -inf alone and, for g, a row
+ * whose token is not in [0, vocab) contribute nothing (zeros); a row whose
+ * log_sum is NaN gets NaN.  row_max, log_sum and entropy are those of the
+ * forward call with the same scale.  dlogits_dev has the logits' dtype, row r
+ * at r * out_stride elements, and may be logits_dev itself (with the same
+ * stride). */
+dobb_status dobb_log_probs_backward(const void* logits_dev, dobb_dtype logits_dtype, int64_t rows,
+                                    int64_t vocab, int64_t row_stride, const void* tokens_dev,
+                                    int token_bytes, float scale, const float* row_max_dev,
+                                    const float* log_sum_dev, const float* entropy_dev,
+                                    const float* grad_logp_dev, const float* grad_entropy_dev,
+                                    const float* grad_lse_dev, void* dlogits_dev,
+                                    int64_t out_stride, void* stream);
+
+/* Embedding lookup: out[t][:] = scale * weight[tokens[t]][:], computed in
+ * fp32 and rounded once to out_dtype.  A token < 0 (padding) and a token >=
+ * vocab give a row of zeros; the latter sets DOBB_FLAG_BAD_TOKEN.
+ *   weight_dev  vocab x dim, row v at v * weight_stride elements
+ *   out_dev     count x dim, row t at t * out_stride elements */
+dobb_status dobb_embedding(const void* weight_dev, dobb_dtype weight_dtype, int64_t vocab,
+                           int64_t dim, int64_t weight_stride, const void* tokens_dev,
+                           int token_bytes, int64_t count, float scale, void* out_dev,
+                           dobb_dtype out_dtype, int64_t out_stride, uint32_t* flags_dev,
+                           void* stream);
+
+/* Bytes of device workspace dobb_embedding_backward needs for `count` tokens
+ * (0 with a message when the sizes are invalid). */
+size_t dobb_embedding_backward_bytes(int64_t count, int64_t vocab, int64_t dim);
+
+/* Gradient of dobb_embedding with respect to the weight:
+ *   dweight[v][:] = scale * sum over t with tokens[t] = v of grad[t][:]
+ * (accumulate 0: every row of dweight is written, zeros for tokens that do not
+ * occur) or added to dweight (accumulate 1: rows of tokens that do not occur
+ * are neither read nor written; the tied embedding adds to the head's
+ * gradient).  The tokens are sorted (stable) and each row's gradients summed
+ * in fp32 in a fixed order that depends only on the tokens; the sum is
+ * rounded once.  Tokens outside [0, vocab) contribute nothing; those >= vocab
+ * set DOBB_FLAG_BAD_TOKEN.  workspace_dev is caller memory of at least
+ * dobb_embedding_backward_bytes(), 256-byte aligned; it holds nothing between
+ * calls.  count is 0 ... 2^31 - 1, vocab 1 ... 2^30. */
+dobb_status dobb_embedding_backward(const void* grad_dev, dobb_dtype grad_dtype, int64_t count,
+                                    int64_t dim, int64_t grad_stride, const void* tokens_dev,
+                                    int token_bytes, int64_t vocab, float scale,
+                                    void* dweight_dev, dobb_dtype dweight_dtype,
+                                    int64_t dweight_stride, int accumulate, uint32_t* flags_dev,
+                                    void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace dobb_clip_grads needs for these tensors (0 with
+ * a message when the sizes are invalid). */
+size_t dobb_clip_grads_bytes(int num_tensors, const int64_t* numel);
+
+/* Global l2 norm of a set of gradients, and clipping by it:
+ *   stats[2 + i] = ||G_i||,  stats[0] = norm = sqrt(sum_i ||G_i||^2)
+ *   stats[1] = c = max_norm / norm if norm > max_norm, else 1
+ *   out_i = c * G_i, rounded once to out_dtype[i]
+ * stats_dev is 2 + num_tensors floats.  No square overflows or underflows on
+ * the way: c is right wherever the norm is finite in 64 bits (a norm beyond
+ * the fp32 range reads Inf in stats).  When an entry is NaN or Inf, norm is
+ * NaN or Inf, DOBB_FLAG_NONFINITE_G is set and c = 1: the gradients are passed
+ * on as they are, and the caller decides.
+ *   G, out     host arrays of device pointers; `out` may be NULL (norms only,
+ *              max_norm is ignored and c = 1); out[i] may be G[i] (in place:
+ *              nothing is written when c = 1) but must not overlap a tensor
+ *              otherwise; an entry with numel 0 may be NULL
+ *   grad_dtype, out_dtype  host arrays of num_tensors dobb_dtype values
+ *   numel      host array of entry counts (0 is allowed), dense tensors
+ *   max_norm   >= 0, not NaN
+ * workspace_dev: at least dobb_clip_grads_bytes(), 256-byte aligned. */
+dobb_status dobb_clip_grads(int num_tensors, const void* const* G, const int32_t* grad_dtype,
+                            const int64_t* numel, float max_norm, void* const* out,
+                            const int32_t* out_dtype, float* stats_dev, uint32_t* flags_dev,
+                            void* workspace_dev, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
