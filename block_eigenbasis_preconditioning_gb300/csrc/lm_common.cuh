@@ -15,6 +15,112 @@ __device__ __forceinline__ int64_t load_token(const void* tokens, int token_byte
                           : static_cast<const int32_t*>(tokens)[i];
 }
 
+// ---- pairs of fp32 values in one 64-bit register (sm_100 packed arithmetic)
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 2^x (a few units of 2^-23 of the result; results below 2^-126 are 0)
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// max that gives NaN if either operand is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 16 bytes of fp32 or bf16 values
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ uint4 fill_neg_inf() {
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
+  // largest of all values of n vectors, NaN if there is one
+  template <int U>
+  static __device__ __forceinline__ float max_of(const uint4 (&v)[U]) {
+    float m = __uint_as_float(v[0].x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m = max_nan(max_nan(max_nan(m, __uint_as_float(v[u].x)), __uint_as_float(v[u].y)),
+                  max_nan(__uint_as_float(v[u].z), __uint_as_float(v[u].w)));
+    }
+    return m;
+  }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ uint64_t pair(const uint4& v, int i) {
+    return i == 0 ? pack2(__uint_as_float(v.x), __uint_as_float(v.y))
+                  : pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ uint4 fill_neg_inf() {
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
+  template <int U>
+  static __device__ __forceinline__ float max_of(const uint4 (&v)[U]) {
+    uint32_t m = v[0].x;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m = max_nan_bf16x2(m, max_nan_bf16x2(max_nan_bf16x2(v[u].x, v[u].y), max_nan_bf16x2(v[u].z, v[u].w)));
+    }
+    return max_nan(bf16_lo(m), bf16_hi(m));
+  }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+    return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+  }
+  static __device__ __forceinline__ uint64_t pair(const uint4& v, int i) {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return pack2(bf16_lo(w), bf16_hi(w));
+  }
+};
+
+// Elements of [p, p + n) before the first 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
+  const int64_t h = (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T);
+  return h < n ? h : n;
+}
+
 inline bool bad_dtype(int d) { return d != DOBB_F32 && d != DOBB_BF16; }
 inline bool misaligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 inline size_t dtype_bytes(int d) { return d == DOBB_F32 ? 4 : 2; }

@@ -7,16 +7,20 @@
 // (M, S, E) of two parts join exactly: with M' the larger maximum and
 // d = scale (M - M'), a part's S becomes S e^d and its E becomes
 // (E + S d) e^d.  An entry -inf adds nothing to either sum.
+#include <cooperative_groups.h>
+
 #include "lm_common.cuh"
 
 namespace dobb {
 namespace {
 
-constexpr int kThreads = 256;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256;  // gradient kernel
 
 struct LpArgs {
   const void* logits;
-  int64_t rows, row_stride;
+  int64_t row_stride;
   int32_t vocab;
   const void* tokens;
   int32_t token_bytes;
@@ -41,29 +45,44 @@ struct LpGradArgs {
   int64_t out_stride;
 };
 
+// ---------------------------------------------------------------- forward
+//
+// A row is read once.  A thread takes 16-byte vectors, kUnroll at a time, and
+// keeps its own (M, S, E); the exponentials are 2^v with v = u log2(e), and E
+// is summed in units of log 2.  An entry far below M is clamped to v = -200,
+// where 2^v is 0, so that -inf adds 0 * -200 and not 0 * -inf.
+//
+// The alternatives cost no second pass: the k-th largest of the 128 segments'
+// maxima (a segment: the entries of kThreads / 128 threads) is a lower bound
+// of the k-th largest entry, so only segments whose maximum reaches it are
+// read again (about k of them, from L2), and their entries that reach it are
+// ranked by counting.  When more entries than the list holds reach the bound
+// (many equal logits), the largest remaining key is searched k times instead.
+
+constexpr int kFwdThreads = 256;
+constexpr int kFwdWarps = kFwdThreads / 32;
+constexpr int kUnroll = 4;
+constexpr int kSegs = 128;
+constexpr int kSegThreads = kFwdThreads / kSegs;
+constexpr int kCand = 256;
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 struct Sums {
-  float m, s, e;
+  float m, s, e;  // e in units of log 2
 };
 
-// A part's contribution at the joint maximum m.  A part that saw only -inf
-// and NaN (m = -inf) holds 0 or NaN in its sums, which pass through.
-__device__ __forceinline__ void add_part(Sums& r, const Sums& a, float scale) {
-  if (a.m == -INFINITY) {
-    r.s += a.s;
-    r.e += a.e;
-  } else {
-    const float d = scale * (a.m - r.m), f = expf(d);
-    r.s += a.s * f;
-    r.e += (f > 0.f) ? (a.e + a.s * d) * f : 0.f;
-  }
-}
-
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float scale) {
-  Sums r{fmaxf(a.m, b.m), 0.f, 0.f};
-  add_part(r, a, scale);
-  add_part(r, b, scale);
-  return r;
-}
+struct FwdShared {
+  Sums part;       // of this CTA's slice of the row
+  unsigned long long best[DOBB_MAX_TOP_K];  // its largest keys, descending; 0 for none
+  float warp_m[kFwdWarps], warp_s[kFwdWarps], warp_e[kFwdWarps];
+  uint32_t seg[kSegs];
+  int32_t seg_list[kSegs];
+  uint32_t bound;
+  int32_t nseg, ncand;
+  unsigned long long cand[kCand];
+  unsigned long long warp_best[kFwdWarps];
+};
 
 // Unsigned integers in the order of the floats; -0 equals 0, every NaN is
 // the largest.
@@ -72,61 +91,127 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+constexpr uint32_t kNegInfKey = 0x007fffffu;
 
+// larger logit first, then lower index
+__device__ __forceinline__ unsigned long long full_key(float x, int32_t j) {
+  return ((unsigned long long)order_key(x) << 32) | (uint32_t)(0x7fffffff - j);
+}
+__device__ __forceinline__ int32_t key_index(unsigned long long k) {
+  return 0x7fffffff - (int32_t)(uint32_t)k;
+}
+
+__device__ __forceinline__ void raise_max(Sums& t, float m, float c) {
+  if (t.m != -INFINITY) {
+    const float d = (t.m - m) * c, f = lm::exp2_fast(d);
+    t.e = (f > 0.f) ? (t.e + t.s * d) * f : 0.f;
+    t.s *= f;
+  }
+  t.m = m;
+}
+
+// The largest top_k keys of the slice x[0 .. n), which starts at index j0 of
+// the row, into sh.best; m is this thread's maximum (NaN if it saw one).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) lp_forward(const LpArgs a) {
-  __shared__ Sums part[kThreads / 32];
-  __shared__ unsigned long long best[kThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    Sums t{-INFINITY, 0.f, 0.f};
-    for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-      const float v = load_f32(x + j);
-      if (v == -INFINITY) continue;
-      if (v > t.m) t = join(t, Sums{v, 0.f, 0.f}, a.scale);
-      const float u = a.scale * (v - t.m), f = expf(u);
-      t.s += f;
-      t.e += (f > 0.f) ? f * u : 0.f;
-    }
+__device__ void slice_top(FwdShared& sh, const T* x, int32_t n, int32_t j0, int32_t head, int32_t nvec,
+                          float m, int top_k) {
+  using V = lm::Vec16<T>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+  uint32_t k = order_key(m);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Sums b;
-      b.m = __shfl_down_sync(0xffffffffu, t.m, o);
-      b.s = __shfl_down_sync(0xffffffffu, t.s, o);
-      b.e = __shfl_down_sync(0xffffffffu, t.e, o);
-      t = join(t, b, a.scale);
-    }
-    __syncthreads();
-    if (lane == 0) part[warp] = t;
-    __syncthreads();
-    Sums r = part[0];
-    for (int w = 1; w < kThreads / 32; ++w) r = join(r, part[w], a.scale);
-    const bool empty = r.m == -INFINITY && r.s == 0.f;
-    const float log_sum = logf(r.s);
-    if (threadIdx.x == 0) {
-      const int64_t tok = lm::load_token(a.tokens, a.token_bytes, row);
-      float lp = 0.f;
-      if (tok >= a.vocab) {
-        lp = NAN;
-        if (a.flags) atomicOr(a.flags, DOBB_FLAG_BAD_TOKEN);
-      } else if (tok >= 0) {
-        const float v = load_f32(x + tok);
-        lp = empty ? -INFINITY : a.scale * (v - r.m) - log_sum;
+  for (int o = 1; o < kSegThreads; o <<= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
+  if (tid % kSegThreads == 0) sh.seg[tid / kSegThreads] = k;
+  if (tid == 0) sh.ncand = 0;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t s[kSegs / 32], keep[kSegs / 32];
+#pragma unroll
+    for (int i = 0; i < kSegs / 32; ++i) keep[i] = s[i] = sh.seg[i * 32 + lane];
+    uint32_t bound = kNegInfKey;
+    for (int r = 0; r < top_k; ++r) {
+      uint32_t b = 0;
+#pragma unroll
+      for (int i = 0; i < kSegs / 32; ++i) b = max(b, s[i]);
+      bound = __reduce_max_sync(0xffffffffu, b);
+      if (bound <= kNegInfKey) break;
+      const unsigned who = __ballot_sync(0xffffffffu, b == bound);
+      if (lane == __ffs(who) - 1) {
+        bool gone = false;
+#pragma unroll
+        for (int i = 0; i < kSegs / 32; ++i) {
+          if (!gone && s[i] == bound) {
+            s[i] = 0;
+            gone = true;
+          }
+        }
       }
-      a.logp[row] = lp;
-      a.row_max[row] = r.m;
-      a.log_sum[row] = log_sum;
-      if (a.lse) a.lse[row] = empty ? -INFINITY : a.scale * r.m + log_sum;
-      if (a.entropy) a.entropy[row] = empty ? 0.f : log_sum - r.e / r.s;
     }
-    // alternatives: the largest key below the last one, top_k times
+    // fewer than top_k segments hold anything above -inf: everything above -inf counts
+    if (bound <= kNegInfKey) bound = kNegInfKey + 1;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kSegs / 32; ++i) {
+      const unsigned who = __ballot_sync(0xffffffffu, keep[i] >= bound);
+      if (keep[i] >= bound) sh.seg_list[at + __popc(who & ((1u << lane) - 1u))] = i * 32 + lane;
+      at += __popc(who);
+    }
+    if (lane == 0) {
+      sh.bound = bound;
+      sh.nseg = at;
+    }
+  }
+  __syncthreads();
+  const uint32_t bound = sh.bound;
+  auto offer = [&](float v, int32_t j) {
+    if (order_key(v) >= bound) {
+      const int at = atomicAdd(&sh.ncand, 1);
+      if (at < kCand) sh.cand[at] = full_key(v, j0 + j);
+    }
+  };
+  for (int q = warp; q < sh.nseg; q += kFwdWarps) {
+    const int first = sh.seg_list[q] * kSegThreads + lane % kSegThreads;
+    for (int32_t j = first + (lane / kSegThreads) * kFwdThreads; j < nvec;
+         j += (32 / kSegThreads) * kFwdThreads) {
+      const uint4 v = xv[j];
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) offer(V::get(v, i), head + j * V::N + i);
+    }
+  }
+  // the entries before and after the vectors
+  if (tid < head) offer(load_f32(x + tid), tid);
+  const int32_t tail0 = head + nvec * V::N;
+  if (tid >= 32 && tid - 32 < n - tail0) offer(load_f32(x + tail0 + tid - 32), tail0 + tid - 32);
+  if (tid < DOBB_MAX_TOP_K) sh.best[tid] = 0;
+  __syncthreads();
+  const int found = sh.ncand;
+  if (found <= kCand) {
+    for (int i = tid; i < found; i += kFwdThreads) {
+      const unsigned long long mine = sh.cand[i];
+      int rank = 0;
+      for (int o = 0; o < found; ++o) rank += sh.cand[o] > mine;
+      if (rank < top_k) sh.best[rank] = mine;
+    }
+    // the rest of the answer is the first -inf entries
+    if (warp == 0 && found < top_k) {
+      int at = found;
+      for (int32_t i = 0; i < n && at < top_k; i += 32) {
+        const bool is = i + lane < n && load_f32(x + i + lane) == -INFINITY;
+        const unsigned who = __ballot_sync(0xffffffffu, is);
+        const int mine = at + __popc(who & ((1u << lane) - 1u));
+        if (is && mine < top_k) sh.best[mine] = full_key(-INFINITY, j0 + i + lane);
+        at += __popc(who);
+      }
+    }
+  } else {
     unsigned long long last = ~0ull;
-    for (int i = 0; i < a.top_k; ++i) {
+    for (int r = 0; r < top_k; ++r) {
       unsigned long long b = 0;
-      for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
-        const unsigned long long key =
-            ((unsigned long long)order_key(load_f32(x + j)) << 32) | (uint32_t)(0x7fffffff - j);
+      for (int32_t j = tid; j < n; j += kFwdThreads) {
+        const unsigned long long key = full_key(load_f32(x + j), j0 + j);
         if (key < last && key > b) b = key;
       }
 #pragma unroll
@@ -134,20 +219,209 @@ __global__ void __launch_bounds__(kThreads) lp_forward(const LpArgs a) {
         const unsigned long long c = __shfl_xor_sync(0xffffffffu, b, o);
         b = c > b ? c : b;
       }
+      if (lane == 0) sh.warp_best[warp] = b;
       __syncthreads();
-      if (lane == 0) best[warp] = b;
-      __syncthreads();
-      b = best[0];
-      for (int w = 1; w < kThreads / 32; ++w) b = best[w] > b ? best[w] : b;
+      b = sh.warp_best[0];
+      for (int w = 1; w < kFwdWarps; ++w) b = sh.warp_best[w] > b ? sh.warp_best[w] : b;
       last = b;
-      if (threadIdx.x == 0) {
-        const int j = 0x7fffffff - (int)(uint32_t)b;
-        a.top_ids[row * a.top_k + i] = j;
-        a.top_logp[row * a.top_k + i] =
-            empty ? -INFINITY : a.scale * (load_f32(x + j) - r.m) - log_sum;
+      if (tid == 0) sh.best[r] = b;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+
+// (M, S, E) and the largest keys of one slice, into sh.part and sh.best
+template <typename T, bool ENT>
+__device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, float c, int top_k) {
+  using V = lm::Vec16<T>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t head = (int32_t)lm::head_of(x, n), nvec = (n - head) / V::N;
+  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+  Sums t{-INFINITY, 0.f, 0.f};
+  bool nan = false;
+  // two sums each, for the even and the odd entries
+  uint64_t s2 = 0, e2 = 0;
+  const uint64_t c2 = lm::pack2(c, c);
+  for (int32_t j = tid; j < nvec; j += kUnroll * kFwdThreads) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      v[u] = j + u * kFwdThreads < nvec ? __ldg(xv + j + u * kFwdThreads) : V::fill_neg_inf();
+    float b = V::max_of(v);
+    if (!(b == b)) {  // the maximum of the others
+      nan = true;
+      b = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) b = fmaxf(b, V::get(v[u], i));
+    }
+    if (b > t.m) {
+      if (t.m != -INFINITY) {
+        const float d = (t.m - b) * c, f = lm::exp2_fast(d);
+        const uint64_t f2 = lm::pack2(f, f);
+        if (ENT) {
+          const float dd = lm::max_nan(d, -200.f);
+          e2 = lm::mul2(lm::fma2(s2, lm::pack2(dd, dd), e2), f2);
+        }
+        s2 = lm::mul2(s2, f2);
+      }
+      t.m = b;
+    }
+    if (t.m == -INFINITY) continue;
+    const uint64_t minus_m = lm::pack2(-t.m, -t.m);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (j + u * kFwdThreads < nvec) {
+#pragma unroll
+        for (int i = 0; i < V::N / 2; ++i) {
+          uint64_t w = lm::mul2(lm::add2(V::pair(v[u], i), minus_m), c2);
+          float a, d;
+          lm::unpack2(w, a, d);
+          if (ENT) {
+            a = lm::max_nan(a, -200.f);
+            d = lm::max_nan(d, -200.f);
+            w = lm::pack2(a, d);
+          }
+          const uint64_t p = lm::pack2(lm::exp2_fast(a), lm::exp2_fast(d));
+          s2 = lm::add2(s2, p);
+          if (ENT) e2 = lm::fma2(p, w, e2);
+        }
       }
     }
   }
+  {
+    float a, b;
+    lm::unpack2(s2, a, b);
+    t.s = a + b;
+    lm::unpack2(e2, a, b);
+    t.e = a + b;
+  }
+  // the entries before and after the vectors: fewer than 8 each
+  {
+    const int32_t tail0 = head + nvec * V::N;
+    const int32_t at = tid < head ? tid : (tid >= 32 && tid - 32 < n - tail0) ? tail0 + tid - 32 : -1;
+    if (at >= 0) {
+      const float v = load_f32(x + at);
+      nan |= !(v == v);
+      if (v > t.m) raise_max(t, v, c);
+      if (t.m != -INFINITY) {
+        const float w = lm::max_nan((v - t.m) * c, -200.f), p = lm::exp2_fast(w);
+        t.s += p;
+        t.e += p * w;
+      }
+    }
+  }
+  if (nan) t.s = NAN;
+  // joint maximum, then the sums relative to it
+  float m = t.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sh.warp_m[warp] = m;
+  __syncthreads();
+  m = sh.warp_m[0];
+#pragma unroll
+  for (int w = 1; w < kFwdWarps; ++w) m = fmaxf(m, sh.warp_m[w]);
+  const float seen = nan ? NAN : t.m;
+  raise_max(t, m, c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+    if (ENT) t.e += __shfl_xor_sync(0xffffffffu, t.e, o);
+  }
+  if (lane == 0) {
+    sh.warp_s[warp] = t.s;
+    sh.warp_e[warp] = t.e;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    Sums r{m, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kFwdWarps; ++w) {
+      r.s += sh.warp_s[w];
+      r.e += sh.warp_e[w];
+    }
+    sh.part = r;
+  }
+  if (top_k > 0) slice_top<T>(sh, x, n, j0, head, nvec, seen, top_k);
+}
+
+// One cluster of CTAs per row (one CTA when the rows fill the GPU): every CTA
+// takes a slice of the row, the first one joins the slices.
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
+  __shared__ FwdShared sh;
+  __shared__ unsigned long long all[kMaxCluster * DOBB_MAX_TOP_K];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t row = blockIdx.x / (unsigned)parts;
+  const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
+  const int32_t per = (int32_t)(((int64_t)a.vocab + parts - 1) / parts);
+  const int32_t lo = (int32_t)min((int64_t)a.vocab, (int64_t)per * rank);
+  const int32_t n = min(a.vocab - lo, per);
+  // the given token's logit is on its way while the row is read
+  int64_t tok = -1;
+  float given = 0.f;
+  if (rank == 0 && threadIdx.x == 0) {
+    tok = lm::load_token(a.tokens, a.token_bytes, row);
+    if (tok >= 0 && tok < a.vocab) given = load_f32(x + tok);
+  }
+  slice_forward<T, ENT>(sh, x + lo, n, lo, a.scale * kLog2e, a.top_k);
+  if (parts > 1) cluster.sync();
+  if (rank == 0) {
+    if (threadIdx.x == 0) {
+      Sums r = sh.part;
+      if (parts > 1) {
+        for (int p = 1; p < parts; ++p) r.m = fmaxf(r.m, cluster.map_shared_rank(&sh, p)->part.m);
+        const float m = r.m;
+        r.s = r.e = 0.f;
+        for (int p = 0; p < parts; ++p) {
+          Sums q = cluster.map_shared_rank(&sh, p)->part;
+          raise_max(q, m, a.scale * kLog2e);
+          r.s += q.s;
+          r.e += q.e;
+        }
+      }
+      const bool empty = r.m == -INFINITY && r.s == 0.f;
+      const float log_sum = logf(r.s);
+      float lp = 0.f;
+      if (tok >= a.vocab) {
+        lp = NAN;
+        if (a.flags) atomicOr(a.flags, DOBB_FLAG_BAD_TOKEN);
+      } else if (tok >= 0) {
+        lp = empty ? -INFINITY : a.scale * (given - r.m) - log_sum;
+      }
+      a.logp[row] = lp;
+      a.row_max[row] = r.m;
+      a.log_sum[row] = log_sum;
+      if (a.lse) a.lse[row] = empty ? -INFINITY : a.scale * r.m + log_sum;
+      if (ENT) a.entropy[row] = empty ? 0.f : log_sum - kLn2 * (r.e / r.s);
+      sh.part = Sums{r.m, log_sum, empty ? 1.f : 0.f};
+    }
+    if (a.top_k > 0) {
+      // the slices' keys: a key's rank among them is its place
+      const int num = parts * a.top_k;
+      for (int i = threadIdx.x; i < num; i += kFwdThreads)
+        all[i] = parts > 1 ? cluster.map_shared_rank(&sh, i / a.top_k)->best[i % a.top_k] : sh.best[i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < num; i += kFwdThreads) {
+        const unsigned long long mine = all[i];
+        int at = i;
+        if (parts > 1) {
+          at = 0;
+          for (int o = 0; o < num; ++o) at += all[o] > mine;
+        }
+        if (mine != 0 && at < a.top_k) {
+          const bool empty = sh.part.e != 0.f;
+          a.top_ids[row * a.top_k + at] = key_index(mine);
+          a.top_logp[row * a.top_k + at] =
+              empty ? -INFINITY : a.scale * (key_value((uint32_t)(mine >> 32)) - sh.part.m) - sh.part.s;
+        }
+      }
+    }
+  }
+  if (parts > 1) cluster.sync();  // the slices' shared memory stays until it was read
 }
 
 template <typename T>
@@ -221,15 +495,36 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
     return fail(DOBB_ERR_INVALID_ARG, "logp, row_max and log_sum must be non-NULL");
   if (top_k > 0 && (!top_ids || !top_logp))
     return fail(DOBB_ERR_INVALID_ARG, "top_ids and top_logp must be non-NULL when top_k > 0");
-  const LpArgs a{logits, rows,    row_stride, (int32_t)vocab, tokens,  token_bytes, scale, top_k,
-                 logp,   lse,     row_max,    log_sum,        entropy, top_ids,     top_logp, flags};
-  const unsigned grid = (unsigned)(rows < (1 << 30) ? rows : (1 << 30));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (logits_dtype == DOBB_F32)
-    lp_forward<float><<<grid, kThreads, 0, s>>>(a);
-  else
-    lp_forward<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  int parts = 1;
+  while (parts < kMaxCluster && rows * parts < 152 && vocab / parts > 4096) parts *= 2;
+  // a launch holds up to 2^31 - 1 blocks
+  const int64_t most = ((int64_t)1 << 30) / parts;
+  cudaError_t e = cudaSuccess;
+  for (int64_t r0 = 0; r0 < rows && e == cudaSuccess; r0 += most) {
+    const int64_t nr = rows - r0 < most ? rows - r0 : most;
+    LpArgs a{static_cast<const char*>(logits) + r0 * row_stride * (int64_t)lm::dtype_bytes(logits_dtype),
+             row_stride, (int32_t)vocab,
+             static_cast<const char*>(tokens) + r0 * token_bytes, token_bytes, scale, top_k, logp + r0,
+             lse ? lse + r0 : nullptr, row_max + r0, log_sum + r0, entropy ? entropy + r0 : nullptr,
+             top_ids ? top_ids + r0 * top_k : nullptr, top_logp ? top_logp + r0 * top_k : nullptr, flags};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(nr * parts));
+    cfg.blockDim = dim3(kFwdThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)parts, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (logits_dtype == DOBB_F32)
+      e = entropy ? cudaLaunchKernelEx(&cfg, lp_forward<float, true>, a)
+                  : cudaLaunchKernelEx(&cfg, lp_forward<float, false>, a);
+    else
+      e = entropy ? cudaLaunchKernelEx(&cfg, lp_forward<__nv_bfloat16, true>, a)
+                  : cudaLaunchKernelEx(&cfg, lp_forward<__nv_bfloat16, false>, a);
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "log-probability launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
 }
