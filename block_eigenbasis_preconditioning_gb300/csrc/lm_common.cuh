@@ -81,6 +81,11 @@ struct Vec16<float> {
     }
     return m;
   }
+  // entries 2 i and 2 i + 1 of a vector
+  static __device__ __forceinline__ void put(uint4& v, int i, float lo, float hi) {
+    (i == 0 ? v.x : v.z) = __float_as_uint(lo);
+    (i == 0 ? v.y : v.w) = __float_as_uint(hi);
+  }
   static __device__ __forceinline__ float get(const uint4& v, int i) {
     return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
   }
@@ -104,6 +109,10 @@ struct Vec16<__nv_bfloat16> {
     }
     return max_nan(bf16_lo(m), bf16_hi(m));
   }
+  static __device__ __forceinline__ void put(uint4& v, int i, float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = *reinterpret_cast<const uint32_t*>(&b);
+  }
   static __device__ __forceinline__ float get(const uint4& v, int i) {
     const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
     return (i & 1) ? bf16_hi(w) : bf16_lo(w);
@@ -119,6 +128,52 @@ template <typename T>
 __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
   const int64_t h = (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T);
   return h < n ? h : n;
+}
+
+// The 16 bytes at p, of which [floor16(p), floor16(p) + 32) may be read: two
+// aligned loads, shifted by the (warp-uniform) misalignment s = p mod 16 > 0.
+__device__ __forceinline__ uint4 load_shifted16(const void* p, uint32_t s) {
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - s);
+  const uint4 a = __ldg(q), b = __ldg(q + 1);
+  uint32_t w[6] = {a.x, a.y, a.z, a.w, b.x, b.y};
+  if (s & 8) {
+    w[0] = a.z;
+    w[1] = a.w;
+    w[2] = b.x;
+    w[3] = b.y;
+    w[4] = b.z;
+    w[5] = b.w;
+  }
+  if (s & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (s & 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The 16 bytes of T at p + i, nothing outside [p, p + n) read; s: the
+// misalignment of p + i, the same for the whole warp.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* p, int64_t i, int64_t n, uint32_t s) {
+  constexpr int N = 16 / (int)sizeof(T);
+  if (s == 0) return __ldg(reinterpret_cast<const uint4*>(p + i));
+  const int64_t before = s / (uint32_t)sizeof(T);
+  if (i >= before && i - before + 2 * N <= n) return load_shifted16(p + i, s);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (sizeof(T) == 4) {
+      w[k] = reinterpret_cast<const uint32_t*>(p + i)[k];
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p + i) + 2 * k;
+      w[k] = h[0] | ((uint32_t)h[1] << 16);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 inline bool bad_dtype(int d) { return d != DOBB_F32 && d != DOBB_BF16; }

@@ -16,8 +16,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;  // gradient kernel
-
 struct LpArgs {
   const void* logits;
   int64_t row_stride;
@@ -43,6 +41,7 @@ struct LpGradArgs {
   const float *g, *h, *l;
   void* out;
   int64_t out_stride;
+  int32_t chunks;  // blocks per row
 };
 
 // ---------------------------------------------------------------- forward
@@ -424,27 +423,83 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
   if (parts > 1) cluster.sync();  // the slices' shared memory stays until it was read
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) lp_backward(const LpGradArgs a) {
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    T* d = static_cast<T*>(a.out) + row * a.out_stride;
-    const float m = a.row_max[row], log_sum = a.log_sum[row];
-    const int64_t tok = lm::load_token(a.tokens, a.token_bytes, row);
-    const bool empty = m == -INFINITY && log_sum == -INFINITY;
-    const float g = (tok >= 0 && tok < a.vocab) ? a.g[row] : 0.f;
-    const float h = a.h ? a.h[row] : 0.f;
-    const float l = a.l ? a.l[row] : 0.f;
-    const float ent = a.h ? a.entropy[row] : 0.f;
-    for (int j = threadIdx.x; j < a.vocab; j += kThreads) {
+// --------------------------------------------------------------- gradient
+//
+// In units of log 2, u_j = scale log2(e) (x_j - M) - log2(S):
+//   p_j = 2^{u_j},  dx_j = p_j (A + B u_j) + scale g [j = t]
+//   A = scale (l - g - h entropy),  B = -scale h ln 2
+// (B = 0 without h).  One block takes kGradVecs vectors per thread of one
+// row, aligned to the output; the logits are shifted into place when the two
+// differ in alignment.  The rows go from the last to the first: a forward
+// call right before leaves the last ones in L2.
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kGradThreads) lp_backward(const LpGradArgs a) {
+  using V = lm::Vec16<T>;
+  const int64_t row = a.rows - 1 - blockIdx.x / (unsigned)a.chunks;
+  const int32_t chunk = blockIdx.x % (unsigned)a.chunks;
+  const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
+  T* d = static_cast<T*>(a.out) + row * a.out_stride;
+  const int32_t head = (int32_t)lm::head_of(d, a.vocab), nvec = (a.vocab - head) / V::N;
+  const uint32_t s = (uint32_t)(reinterpret_cast<uintptr_t>(x + head) & 15);
+  const int32_t v0 = chunk * (kGradThreads * kGradVecs) + threadIdx.x;
+  uint4 v[kGradVecs];
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u) {
+    const int32_t j = v0 + u * kGradThreads;
+    if (j < nvec) v[u] = lm::load16(x, (int64_t)head + (int64_t)j * V::N, a.vocab, s);
+  }
+  const float m = a.row_max[row], log_sum = a.log_sum[row];
+  const int64_t tok = lm::load_token(a.tokens, a.token_bytes, row);
+  const bool empty = m == -INFINITY && log_sum == -INFINITY;
+  const float g = (tok >= 0 && tok < a.vocab) ? a.scale * a.g[row] : 0.f;
+  const float h = ENT ? a.scale * a.h[row] : 0.f;
+  const float l = a.l ? a.scale * a.l[row] : 0.f;
+  const float A = ENT ? l - g - h * a.entropy[row] : l - g, B = -h * kLn2;
+  const float c = a.scale * kLog2e, log2_sum = log_sum * kLog2e;
+  const uint64_t minus_m = lm::pack2(-m, -m), c2 = lm::pack2(c, c),
+                 minus_s = lm::pack2(-log2_sum, -log2_sum), A2 = lm::pack2(A, A), B2 = lm::pack2(B, B);
+  const int32_t tok_vec = (tok >= head && tok < a.vocab) ? (int32_t)((tok - head) / V::N) : -1;
+#pragma unroll
+  for (int u = 0; u < kGradVecs; ++u) {
+    const int32_t j = v0 + u * kGradThreads;
+    if (j >= nvec) break;
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (!empty) {
+#pragma unroll
+      for (int i = 0; i < V::N / 2; ++i) {
+        uint64_t w = lm::fma2(lm::add2(V::pair(v[u], i), minus_m), c2, minus_s);
+        float lo, hi;
+        lm::unpack2(w, lo, hi);
+        if (ENT) {  // p u is 0, not 0 * -inf, where p is 0
+          lo = lm::max_nan(lo, -200.f);
+          hi = lm::max_nan(hi, -200.f);
+          w = lm::pack2(lo, hi);
+        }
+        const uint64_t p = lm::pack2(lm::exp2_fast(lo), lm::exp2_fast(hi));
+        lm::unpack2(lm::mul2(p, ENT ? lm::fma2(B2, w, A2) : A2), lo, hi);
+        if (j == tok_vec) {
+          if (head + j * V::N + 2 * i == tok) lo += g;
+          if (head + j * V::N + 2 * i + 1 == tok) hi += g;
+        }
+        V::put(o, i, lo, hi);
+      }
+    }
+    __stcs(reinterpret_cast<uint4*>(d + head) + j, o);
+  }
+  if (chunk == 0) {  // the entries before and after the vectors: fewer than 8 each
+    const int32_t tail0 = head + nvec * V::N;
+    const int32_t tid = threadIdx.x;
+    const int32_t j = tid < head ? tid : (tid >= 32 && tid - 32 < a.vocab - tail0) ? tail0 + tid - 32 : -1;
+    if (j >= 0) {
       float r = 0.f;
       if (!empty) {
-        const float lp = a.scale * (load_f32(x + j) - m) - log_sum;
-        const float p = expf(lp);
-        if (p != 0.f) r = p * (l - g - h * (lp + ent));
-        if (j == tok) r += g;
+        const float w = lm::max_nan(fmaf(load_f32(x + j) - m, c, -log2_sum), -200.f);
+        r = lm::exp2_fast(w) * fmaf(B, w, A) + (j == tok ? g : 0.f);
       }
-      store_f32(d + j, a.scale * r);
+      store_f32(d + j, r);
     }
   }
 }
@@ -551,16 +606,43 @@ extern "C" dobb_status dobb_log_probs_backward(const void* logits, dobb_dtype lo
     return fail(DOBB_ERR_INVALID_ARG, "dlogits not aligned to its element size");
   if (dlogits == logits && out_stride != row_stride && rows > 1)
     return fail(DOBB_ERR_INVALID_ARG, "in place the strides must be equal");
-  const LpGradArgs a{logits,  rows,    row_stride, (int32_t)vocab, tokens,       token_bytes, scale,
-                     row_max, log_sum, entropy,    grad_logp,      grad_entropy, grad_lse,    dlogits,
-                     out_stride};
-  const unsigned grid = (unsigned)(rows < (1 << 30) ? rows : (1 << 30));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (logits_dtype == DOBB_F32)
-    lp_backward<float><<<grid, kThreads, 0, s>>>(a);
-  else
-    lp_backward<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const int64_t per = (int64_t)kGradThreads * kGradVecs * (16 / (int64_t)lm::dtype_bytes(logits_dtype));
+  const int64_t chunks = (vocab + per - 1) / per, most = ((int64_t)1 << 30) / chunks;
+  const size_t bytes = lm::dtype_bytes(logits_dtype);
+  cudaError_t e = cudaSuccess;
+  for (int64_t end = rows; end > 0 && e == cudaSuccess; end -= most) {  // the last rows first
+    const int64_t r0 = end > most ? end - most : 0;
+    const LpGradArgs a{static_cast<const char*>(logits) + r0 * row_stride * (int64_t)bytes,
+                       end - r0,
+                       row_stride,
+                       (int32_t)vocab,
+                       static_cast<const char*>(tokens) + r0 * token_bytes,
+                       token_bytes,
+                       scale,
+                       row_max + r0,
+                       log_sum + r0,
+                       entropy ? entropy + r0 : nullptr,
+                       grad_logp + r0,
+                       grad_entropy ? grad_entropy + r0 : nullptr,
+                       grad_lse ? grad_lse + r0 : nullptr,
+                       static_cast<char*>(dlogits) + r0 * out_stride * (int64_t)bytes,
+                       out_stride,
+                       (int32_t)chunks};
+    const unsigned grid = (unsigned)((end - r0) * chunks);
+    if (logits_dtype == DOBB_F32) {
+      if (grad_entropy)
+        lp_backward<float, true><<<grid, kGradThreads, 0, s>>>(a);
+      else
+        lp_backward<float, false><<<grid, kGradThreads, 0, s>>>(a);
+    } else {
+      if (grad_entropy)
+        lp_backward<__nv_bfloat16, true><<<grid, kGradThreads, 0, s>>>(a);
+      else
+        lp_backward<__nv_bfloat16, false><<<grid, kGradThreads, 0, s>>>(a);
+    }
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess)
     return fail(DOBB_ERR_CUDA, "log-probability gradient launch: %s", cudaGetErrorString(e));
   return DOBB_OK;

@@ -17,6 +17,7 @@ Wrong arguments raise ValueError before anything is launched.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -51,78 +52,96 @@ class GradNorm(NamedTuple):
     norms: torch.Tensor
 
 
-def _need(ok: bool, msg: str, *args) -> None:
-    if not ok:
-        raise ValueError(msg.format(*args))
+# A serving call on a few rows takes the GPU microseconds, so the checks below
+# are plain comparisons and the raw stream is read without a Stream object
+# (0.1 us against 2 us); messages are built only when a check fails.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _device_of(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
-    dev = first.device
-    _need(dev.type == "cuda", "tensors must be on a CUDA device, got {}", dev)
+def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """Index of the CUDA device that all of the tensors are on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {first.device}")
     for t in others:
-        _need(t is None or t.device == dev, "all tensors must be on {}", dev)
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on {first.device}, got one on {t.device}")
+    return index
+
+
+class _On:
+    """Device and stream of a call that is not on the current ones: what is
+    allocated inside comes from that stream, and the tensors it uses outlive
+    the work on it."""
+
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream], used):
+        if stream is None:
+            self.ctx = torch.cuda.device(index)
+        else:
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+            self.ctx = torch.cuda.stream(stream)
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        self.ctx.__exit__(*exc)
+
+
+def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]) -> bool:
+    return stream is not None or index != torch.cuda.current_device()
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Row stride of a matrix whose rows are contiguous."""
-    _need(t.dim() == 2, "{} must be a matrix, got {} dimensions", name, t.dim())
-    _need(t.stride(1) == 1 or t.shape[1] <= 1, "{} must have contiguous rows", name)
-    _need(t.stride(0) >= t.shape[1] or t.shape[0] <= 1, "{} must not overlap itself", name)
-    return max(t.stride(0), t.shape[1])
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    rows, cols = t.shape
+    down, across = t.stride()
+    if across != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if down < cols:
+        if rows > 1:
+            raise ValueError(f"{name} must not overlap itself")
+        return cols
+    return down
 
 
-def _tokens(t: torch.Tensor, name: str) -> int:
-    _need(t.dtype in _TOKEN_BYTES, "{} must be int32 or int64, got {}", name, t.dtype)
-    _need(t.is_contiguous(), "{} must be contiguous", name)
-    return _TOKEN_BYTES[t.dtype]
+def _token_bytes(t: torch.Tensor) -> int:
+    size = _TOKEN_BYTES.get(t.dtype)
+    if size is None:
+        raise ValueError(f"tokens must be int32 or int64, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    return size
 
 
 def _vector(t: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
     if t is None:
         return None
-    _need(t.dtype == torch.float32 and t.is_contiguous() and t.numel() == n,
-          "{} must be {} contiguous float32 values", name, n)
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be {n} contiguous float32 values")
     return t.data_ptr()
 
 
 def _flags(flags: Optional[torch.Tensor]) -> Optional[int]:
     if flags is None:
         return None
-    _need(flags.dtype in (torch.int32, torch.uint32) and flags.numel() == 1,
-          "flags must be one int32 or uint32")
+    if flags.dtype not in (torch.int32, torch.uint32) or flags.numel() != 1:
+        raise ValueError("flags must be one int32 or uint32")
     return flags.data_ptr()
 
 
 def _float_dtype(dtype: torch.dtype, name: str) -> int:
-    _need(dtype in _DTYPES, "{} must be float32 or bfloat16, got {}", name, dtype)
-    return _DTYPES[dtype]
-
-
-class _On:
-    """The device and stream of a call: allocations inside come from that
-    stream, and inputs made on another stream outlive the work on it."""
-
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream], used):
-        self.ctx = []
-        if stream is not None and stream != torch.cuda.current_stream(device):
-            _need(stream.device == device, "the stream is on {}, the tensors on {}", stream.device, device)
-            self.ctx.append(torch.cuda.stream(stream))
-            for t in used:
-                if t is not None:
-                    t.record_stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
-        self.ptr = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return self.ptr
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return code
 
 
 # ------------------------------------------------------------ log probabilities
@@ -139,21 +158,29 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
     stride = _rows(logits, "logits")
     dtype = _float_dtype(logits.dtype, "logits")
     rows, vocab = logits.shape
-    token_bytes = _tokens(tokens, "tokens")
-    _need(tokens.numel() == rows, "{} tokens for {} rows", tokens.numel(), rows)
-    _need(0 <= top_k <= min(MAX_TOP_K, vocab), "top_k must lie in [0, min({}, vocab)], got {}", MAX_TOP_K, top_k)
-    dev = _device_of(logits, tokens, flags)
-    lib = load_library()
-    with _On(dev, stream, (logits, tokens, flags)) as s:
-        f = torch.empty(5 if entropy else 4, rows, dtype=torch.float32, device=dev)
-        ids = torch.empty(rows, top_k, dtype=torch.int32, device=dev) if top_k else None
-        alt = torch.empty(rows, top_k, dtype=torch.float32, device=dev) if top_k else None
-        p = f.data_ptr()
-        check(lib.dobb_log_probs(
-            logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes, scale, top_k, p, p + 4 * rows,
-            p + 8 * rows, p + 12 * rows, p + 16 * rows if entropy else None, ids.data_ptr() if top_k else None,
-            alt.data_ptr() if top_k else None, _flags(flags), s))
-    return LogProbs(f[0], f[1], f[4] if entropy else None, ids, alt, f[2], f[3], float(scale))
+    token_bytes = _token_bytes(tokens)
+    if tokens.numel() != rows:
+        raise ValueError(f"{tokens.numel()} tokens for {rows} rows")
+    if not 0 <= top_k <= min(MAX_TOP_K, vocab):
+        raise ValueError(f"top_k must lie in [0, min({MAX_TOP_K}, vocab)], got {top_k}")
+    index = _device(logits, tokens, flags)
+    if _elsewhere(index, stream):
+        with _On(index, stream, (logits, tokens, flags)):
+            return log_probs(logits, tokens, scale=scale, top_k=top_k, entropy=entropy, flags=flags)
+    dev = logits.device
+    # logp, lse, row_max, log_sum (, entropy): rows of one allocation
+    f = torch.empty((5 if entropy else 4, rows), dtype=torch.float32, device=dev)
+    p, ids, alt, ids_p, alt_p = f.data_ptr(), None, None, None, None
+    if top_k:
+        ids = torch.empty((rows, top_k), dtype=torch.int32, device=dev)
+        alt = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
+        ids_p, alt_p = ids.data_ptr(), alt.data_ptr()
+    n = 4 * rows
+    check(load_library().dobb_log_probs(
+        logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes, scale, top_k, p, p + n, p + 2 * n,
+        p + 3 * n, p + 4 * n if entropy else None, ids_p, alt_p, _flags(flags), _raw_stream(index)))
+    logp, lse, row_max, log_sum, *ent = f.unbind(0)
+    return LogProbs(logp, lse, ent[0] if entropy else None, ids, alt, row_max, log_sum, float(scale))
 
 
 def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogProbs, grad_logp: torch.Tensor, *,
@@ -165,22 +192,27 @@ def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogPr
     stride = _rows(logits, "logits")
     dtype = _float_dtype(logits.dtype, "logits")
     rows, vocab = logits.shape
-    token_bytes = _tokens(tokens, "tokens")
-    _need(tokens.numel() == rows, "{} tokens for {} rows", tokens.numel(), rows)
-    _need(grad_entropy is None or result.entropy is not None, "grad_entropy needs a result with the entropy")
-    dev = _device_of(logits, tokens, grad_logp, grad_entropy, grad_lse, out, result.row_max)
+    token_bytes = _token_bytes(tokens)
+    if tokens.numel() != rows:
+        raise ValueError(f"{tokens.numel()} tokens for {rows} rows")
+    if grad_entropy is not None and result.entropy is None:
+        raise ValueError("grad_entropy needs a result with the entropy")
+    index = _device(logits, tokens, grad_logp, grad_entropy, grad_lse, out, result.row_max)
+    if _elsewhere(index, stream):
+        with _On(index, stream, (logits, tokens, out, grad_logp, grad_entropy, grad_lse, result.row_max, result.log_sum,
+                                 result.entropy)):
+            return log_probs_backward(logits, tokens, result, grad_logp, grad_entropy=grad_entropy, grad_lse=grad_lse, out=out)
     args = [_vector(result.row_max, rows, "row_max"), _vector(result.log_sum, rows, "log_sum"),
             _vector(result.entropy if grad_entropy is not None else None, rows, "entropy"),
             _vector(grad_logp, rows, "grad_logp"), _vector(grad_entropy, rows, "grad_entropy"),
             _vector(grad_lse, rows, "grad_lse")]
-    lib = load_library()
-    with _On(dev, stream, (logits, tokens, out, grad_logp, grad_entropy, grad_lse, result.row_max, result.log_sum,
-                           result.entropy)) as s:
-        if out is None:
-            out = torch.empty(rows, vocab, dtype=logits.dtype, device=dev)
-        _need(out.shape == logits.shape and out.dtype == logits.dtype, "out must have the logits' shape and dtype")
-        check(lib.dobb_log_probs_backward(logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes,
-                                          result.scale, *args, out.data_ptr(), _rows(out, "out"), s))
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and dtype")
+    check(load_library().dobb_log_probs_backward(
+        logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes, result.scale, *args, out.data_ptr(),
+        _rows(out, "out"), _raw_stream(index)))
     return out
 
 
@@ -197,21 +229,25 @@ def embedding(weight: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
     wstride = _rows(weight, "weight")
     wdtype = _float_dtype(weight.dtype, "weight")
     vocab, dim = weight.shape
-    token_bytes = _tokens(tokens, "tokens")
+    token_bytes = _token_bytes(tokens)
     count = tokens.numel()
-    _need(out is None or out_dtype in (None, out.dtype), "out has dtype {}", out.dtype if out is not None else None)
+    if out is not None and out_dtype not in (None, out.dtype):
+        raise ValueError(f"out has dtype {out.dtype}")
     odtype = _float_dtype(out.dtype if out is not None else (out_dtype or weight.dtype), "out dtype")
-    dev = _device_of(weight, tokens, out, flags)
-    lib = load_library()
-    with _On(dev, stream, (weight, tokens, out, flags)) as s:
-        if out is None:
-            out = torch.empty(tokens.shape + (dim,), dtype=out_dtype or weight.dtype, device=dev)
-            ostride = dim
-        else:
-            ostride = _rows(out, "out")
-            _need(tuple(out.shape) == (count, dim), "out must be {} x {}", count, dim)
-        check(lib.dobb_embedding(weight.data_ptr(), wdtype, vocab, dim, wstride, tokens.data_ptr(), token_bytes, count, scale,
-                                 out.data_ptr(), odtype, ostride, _flags(flags), s))
+    index = _device(weight, tokens, out, flags)
+    if _elsewhere(index, stream):
+        with _On(index, stream, (weight, tokens, out, flags)):
+            return embedding(weight, tokens, scale=scale, out_dtype=out_dtype, out=out, flags=flags)
+    if out is None:
+        out = torch.empty((*tokens.shape, dim), dtype=out_dtype or weight.dtype, device=weight.device)
+        ostride = dim
+    else:
+        ostride = _rows(out, "out")
+        if out.shape != (count, dim):
+            raise ValueError(f"out must be {count} x {dim}")
+    check(load_library().dobb_embedding(
+        weight.data_ptr(), wdtype, vocab, dim, wstride, tokens.data_ptr(), token_bytes, count, scale, out.data_ptr(), odtype,
+        ostride, _flags(flags), _raw_stream(index)))
     return out
 
 
@@ -224,35 +260,43 @@ def embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: Optional
 
     grad: tokens.shape + (dim,) contiguous, or a (tokens, dim) matrix with
     contiguous rows; `out`: (vocab, dim) with contiguous rows."""
-    token_bytes = _tokens(tokens, "tokens")
+    token_bytes = _token_bytes(tokens)
     count = tokens.numel()
-    _need(grad.dim() >= 1, "grad must have a last dimension")
+    if grad.dim() < 1 or grad.numel() != count * grad.shape[-1]:
+        raise ValueError(f"grad of shape {tuple(grad.shape)} for {count} tokens")
     dim = grad.shape[-1]
-    _need(grad.numel() == count * dim, "grad has {} values for {} tokens of {}", grad.numel(), count, dim)
     if grad.dim() != 2:
-        _need(grad.is_contiguous(), "grad must be contiguous, or a matrix")
+        if not grad.is_contiguous():
+            raise ValueError("grad must be contiguous, or a matrix")
         grad = grad.view(count, dim)
-    _need(grad.shape[0] == count, "grad has {} rows for {} tokens", grad.shape[0], count)
+    if grad.shape[0] != count:
+        raise ValueError(f"grad has {grad.shape[0]} rows for {count} tokens")
     gstride = _rows(grad, "grad")
     gdtype = _float_dtype(grad.dtype, "grad")
-    _need(out is not None or not accumulate, "accumulate needs out")
-    _need(out is not None or vocab is not None, "vocab or out must be given")
-    _need(out is None or dtype in (None, out.dtype), "out has dtype {}", out.dtype if out is not None else None)
-    dev = _device_of(grad, tokens, out, flags)
+    if out is None:
+        if accumulate or vocab is None:
+            raise ValueError("accumulate needs out" if accumulate else "vocab or out must be given")
+    else:
+        if dtype not in (None, out.dtype):
+            raise ValueError(f"out has dtype {out.dtype}")
+        if out.dim() != 2 or out.shape[1] != dim or (vocab is not None and out.shape[0] != vocab):
+            raise ValueError(f"out must be {'vocab' if vocab is None else vocab} x {dim}")
+        vocab = out.shape[0]
+    odtype = _float_dtype(out.dtype if out is not None else (dtype or grad.dtype), "out dtype")
+    index = _device(grad, tokens, out, flags)
+    if _elsewhere(index, stream):
+        with _On(index, stream, (grad, tokens, out, flags)):
+            return embedding_backward(grad, tokens, vocab, scale=scale, dtype=dtype, out=out, accumulate=accumulate, flags=flags)
     lib = load_library()
-    with _On(dev, stream, (grad, tokens, out, flags)) as s:
-        if out is None:
-            out = torch.empty(int(vocab), dim, dtype=dtype or grad.dtype, device=dev)
-        _need(out.dim() == 2 and out.shape[1] == dim and (vocab is None or out.shape[0] == vocab),
-              "out must be {} x {}", vocab if vocab is not None else "vocab", dim)
-        odtype = _float_dtype(out.dtype, "out dtype")
-        nbytes = lib.dobb_embedding_backward_bytes(count, out.shape[0], dim)
-        if nbytes == 0:
-            check(1)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        check(lib.dobb_embedding_backward(grad.data_ptr(), gdtype, count, dim, gstride, tokens.data_ptr(), token_bytes,
-                                          out.shape[0], scale, out.data_ptr(), odtype, _rows(out, "out"), int(accumulate),
-                                          _flags(flags), ws.data_ptr(), nbytes, s))
+    nbytes = lib.dobb_embedding_backward_bytes(count, vocab, dim)
+    if nbytes == 0:
+        check(1)
+    if out is None:
+        out = torch.empty((vocab, dim), dtype=dtype or grad.dtype, device=grad.device)
+    ws = torch.empty((nbytes,), dtype=torch.uint8, device=grad.device)
+    check(lib.dobb_embedding_backward(
+        grad.data_ptr(), gdtype, count, dim, gstride, tokens.data_ptr(), token_bytes, vocab, scale, out.data_ptr(), odtype,
+        _rows(out, "out"), int(accumulate), _flags(flags), ws.data_ptr(), nbytes, _raw_stream(index)))
     return out
 
 
@@ -270,44 +314,65 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+def _dtype_codes(tensors, what: str):
+    try:
+        return array("i", [_DTYPES[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise ValueError(f"every {what} must be float32 or bfloat16, got {e.args[0]}") from None
+
+
+def _at(a: array, kind):
+    """A ctypes pointer to an array's values."""
+    return ctypes.cast(a.buffer_info()[0], ctypes.POINTER(kind))
+
+
 def _clip(grads: Sequence[torch.Tensor], max_norm: float, outs: Optional[Sequence[torch.Tensor]],
           flags: Optional[torch.Tensor], stream: Optional[torch.cuda.Stream]) -> GradNorm:
-    grads = list(grads)
     n = len(grads)
-    _need(n > 0, "no gradients given")
-    _need(outs is None or len(outs) == n, "{} outputs for {} gradients", 0 if outs is None else len(outs), n)
-    dev = _device_of(*grads, flags)
-    for i, g in enumerate(grads):
-        _need(g.dtype in _DTYPES, "gradient {} must be float32 or bfloat16, got {}", i, g.dtype)
-        _need(_dense(g), "gradient {} must be dense", i)
-    if outs is not None and outs is not grads:
-        _device_of(grads[0], *outs)
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            _need(o.dtype in _DTYPES, "output {} must be float32 or bfloat16, got {}", i, o.dtype)
-            _need(o.shape == g.shape and (o.stride() == g.stride() or (o.is_contiguous() and g.is_contiguous())),
-                  "output {} must have its gradient's shape and strides", i)
+    if n == 0:
+        raise ValueError("no gradients given")
+    in_place = outs is grads
+    index = _device(*grads, flags)
+    gd = _dtype_codes(grads, "gradient")
+    plain = all(map(torch.Tensor.is_contiguous, grads))
+    if not plain and not all(map(_dense, grads)):
+        raise ValueError("every gradient must be dense")
+    od = gd
+    if outs is not None and not in_place:
+        if len(outs) != n:
+            raise ValueError(f"{len(outs)} outputs for {n} gradients")
+        _device(grads[0], *outs)
+        od = _dtype_codes(outs, "output")
+        if not all(g.shape == o.shape for g, o in zip(grads, outs)):
+            raise ValueError("every output must have its gradient's shape")
+        if not (plain and all(map(torch.Tensor.is_contiguous, outs))) and not all(
+                g.stride() == o.stride() or (g.is_contiguous() and o.is_contiguous()) for g, o in zip(grads, outs)):
+            raise ValueError("every output must have its gradient's strides")
+    if _elsewhere(index, stream):
+        with _On(index, stream, [*grads, *(outs or ()), flags]):
+            return _clip(grads, max_norm, outs, flags, None)
     lib = load_library()
-    gp = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    gd = (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads])
-    ne = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    op = od = None
-    if outs is not None:
-        op = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
-        od = (ctypes.c_int32 * n)(*[_DTYPES[o.dtype] for o in outs])
-    nbytes = lib.dobb_clip_grads_bytes(n, ne)
+    gp = array("Q", map(torch.Tensor.data_ptr, grads))
+    ne = array("q", map(torch.Tensor.numel, grads))
+    op = None if outs is None else gp if in_place else array("Q", map(torch.Tensor.data_ptr, outs))
+    sizes = _at(ne, ctypes.c_int64)
+    nbytes = lib.dobb_clip_grads_bytes(n, sizes)
     if nbytes == 0:
         check(1)
-    with _On(dev, stream, [*grads, *(outs or ()), flags]) as s:
-        stats = torch.empty(2 + n, dtype=torch.float32, device=dev)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        check(lib.dobb_clip_grads(n, gp, gd, ne, max_norm, op, od, stats.data_ptr(), _flags(flags), ws.data_ptr(), nbytes, s))
+    dev = grads[0].device
+    stats = torch.empty((2 + n,), dtype=torch.float32, device=dev)
+    ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    check(lib.dobb_clip_grads(
+        n, _at(gp, ctypes.c_void_p), _at(gd, ctypes.c_int32), sizes, max_norm, None if op is None else _at(op, ctypes.c_void_p),
+        None if op is None else _at(od, ctypes.c_int32), stats.data_ptr(), _flags(flags), ws.data_ptr(), nbytes,
+        _raw_stream(index)))
     return GradNorm(stats[0], stats[1], stats[2:])
 
 
 def grad_norm(grads: Sequence[torch.Tensor], *, flags: Optional[torch.Tensor] = None,
               stream: Optional[torch.cuda.Stream] = None) -> GradNorm:
     """The l2 norm over all entries of all gradients, and each tensor's own."""
-    return _clip(grads, 0.0, None, flags, stream)
+    return _clip(list(grads), 0.0, None, flags, stream)
 
 
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
@@ -319,6 +384,7 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[
     on unscaled and flag 2 (non-finite gradient) is set in `flags`.
 
     grads: float32 or bfloat16 tensors, mixed if need be, of any shapes."""
-    _need(max_norm >= 0, "max_norm must be >= 0, got {}", max_norm)
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm must be >= 0, got {max_norm}")
     grads = list(grads)
     return _clip(grads, float(max_norm), grads if out is None else list(out), flags, stream)
