@@ -9,6 +9,8 @@
 // (E + S d) e^d.  An entry -inf adds nothing to either sum.
 #include <cooperative_groups.h>
 
+#include <cfloat>
+
 #include "lm_common.cuh"
 
 namespace dobb {
@@ -47,9 +49,13 @@ struct LpGradArgs {
 // ---------------------------------------------------------------- forward
 //
 // A row is read once.  A thread takes 16-byte vectors, kUnroll at a time, and
-// keeps its own (M, S, E); the exponentials are 2^v with v = u log2(e), and E
-// is summed in units of log 2.  An entry far below M is clamped to v = -200,
-// where 2^v is 0, so that -inf adds 0 * -200 and not 0 * -inf.
+// keeps its own maximum M and sums S, E; the exponentials are 2^v, and E is
+// summed in units of log 2.  v = x c - R, c = scale log2(e), is one fused
+// multiply-add: the reference R is M c rounded, and taken as exact from there
+// on, so the rounding costs nothing.  An entry far below M is clamped to
+// v = -200, where 2^v is 0, so that -inf adds 0 * -200 and not 0 * -inf.
+// Where M c leaves the range of fp32 (masks of the type's lowest value and
+// nothing else in the row) the slice is summed again as 2^{(x - M) c}.
 //
 // The alternatives cost no second pass: the k-th largest of the 128 segments'
 // maxima (a segment: the entries of kThreads / 128 threads) is a lower bound
@@ -68,7 +74,8 @@ constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Sums {
-  float m, s, e;  // e in units of log 2
+  float m, r;  // the maximum, and what s and e refer to
+  float s, e;  // e in units of log 2
 };
 
 struct FwdShared {
@@ -103,13 +110,15 @@ __device__ __forceinline__ int32_t key_index(unsigned long long k) {
   return 0x7fffffff - (int32_t)(uint32_t)k;
 }
 
-__device__ __forceinline__ void raise_max(Sums& t, float m, float c) {
-  if (t.m != -INFINITY) {
-    const float d = (t.m - m) * c, f = lm::exp2_fast(d);
-    t.e = (f > 0.f) ? (t.e + t.s * d) * f : 0.f;
-    t.s *= f;
-  }
-  t.m = m;
+// R of a maximum; a slice of -inf alone, or of values whose product with c
+// overflows, gets the lowest number
+__device__ __forceinline__ float reference(float m, float c) { return fmaxf(m * c, -FLT_MAX); }
+
+// the sums relative to a larger reference
+__device__ __forceinline__ void raise_to(float& s, float& e, float from, float to) {
+  const float d = lm::max_nan(from - to, -1000.f), f = lm::exp2_fast(d);
+  e = (e + s * d) * f;
+  s *= f;
 }
 
 // The largest top_k keys of the slice x[0 .. n), which starts at index j0 of
@@ -175,9 +184,10 @@ __device__ void slice_top(FwdShared& sh, const T* x, int32_t n, int32_t j0, int3
     const int first = sh.seg_list[q] * kSegThreads + lane % kSegThreads;
     for (int32_t j = first + (lane / kSegThreads) * kFwdThreads; j < nvec;
          j += (32 / kSegThreads) * kFwdThreads) {
-      const uint4 v = xv[j];
+      const uint4 v[1] = {xv[j]};
+      if (order_key(V::max_of(v)) < bound) continue;
 #pragma unroll
-      for (int i = 0; i < V::N; ++i) offer(V::get(v, i), head + j * V::N + i);
+      for (int i = 0; i < V::N; ++i) offer(V::get(v[0], i), head + j * V::N + i);
     }
   }
   // the entries before and after the vectors
@@ -230,72 +240,77 @@ __device__ void slice_top(FwdShared& sh, const T* x, int32_t n, int32_t j0, int3
   __syncthreads();
 }
 
-// (M, S, E) and the largest keys of one slice, into sh.part and sh.best
+// The vectors v of a thread onto its maximum and sums (s2, e2: two sums each,
+// for the even and the odd entries)
+template <typename T, bool ENT, int U>
+__device__ __forceinline__ void add_vectors(const uint4 (&v)[U], float c, uint64_t c2, float& m, float& r,
+                                            uint64_t& s2, uint64_t& e2, bool& nan) {
+  using V = lm::Vec16<T>;
+  float b = V::max_of(v);
+  if (!(b == b)) {  // the maximum of the others
+    nan = true;
+    b = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) b = fmaxf(b, V::get(v[u], i));
+  }
+  if (b > m) {
+    m = b;
+    const float to = reference(b, c), d = lm::max_nan(r - to, -1000.f), f = lm::exp2_fast(d);
+    const uint64_t f2 = lm::pack2(f, f);
+    if (ENT) e2 = lm::mul2(lm::fma2(s2, lm::pack2(d, d), e2), f2);
+    s2 = lm::mul2(s2, f2);
+    r = to;
+  }
+  const uint64_t minus_r = lm::pack2(-r, -r);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < V::N / 2; ++i) {
+      uint64_t w = lm::fma2(V::pair(v[u], i), c2, minus_r);
+      float lo, hi;
+      lm::unpack2(w, lo, hi);
+      if (ENT) {
+        lo = lm::max_nan(lo, -200.f);
+        hi = lm::max_nan(hi, -200.f);
+        w = lm::pack2(lo, hi);
+      }
+      const uint64_t p = lm::pack2(lm::exp2_fast(lo), lm::exp2_fast(hi));
+      s2 = lm::add2(s2, p);
+      if (ENT) e2 = lm::fma2(p, w, e2);
+    }
+  }
+}
+
+// Maximum, sums and the largest keys of one slice, into sh.part and sh.best
 template <typename T, bool ENT>
 __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, float c, int top_k) {
   using V = lm::Vec16<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t head = (int32_t)lm::head_of(x, n), nvec = (n - head) / V::N;
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  Sums t{-INFINITY, 0.f, 0.f};
+  float own = -INFINITY, r = -FLT_MAX, s, e;
   bool nan = false;
-  // two sums each, for the even and the odd entries
   uint64_t s2 = 0, e2 = 0;
   const uint64_t c2 = lm::pack2(c, c);
-  for (int32_t j = tid; j < nvec; j += kUnroll * kFwdThreads) {
+  int32_t j = tid;
+  for (; j + (kUnroll - 1) * kFwdThreads < nvec; j += kUnroll * kFwdThreads) {
     uint4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      v[u] = j + u * kFwdThreads < nvec ? __ldg(xv + j + u * kFwdThreads) : V::fill_neg_inf();
-    float b = V::max_of(v);
-    if (!(b == b)) {  // the maximum of the others
-      nan = true;
-      b = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < V::N; ++i) b = fmaxf(b, V::get(v[u], i));
-    }
-    if (b > t.m) {
-      if (t.m != -INFINITY) {
-        const float d = (t.m - b) * c, f = lm::exp2_fast(d);
-        const uint64_t f2 = lm::pack2(f, f);
-        if (ENT) {
-          const float dd = lm::max_nan(d, -200.f);
-          e2 = lm::mul2(lm::fma2(s2, lm::pack2(dd, dd), e2), f2);
-        }
-        s2 = lm::mul2(s2, f2);
-      }
-      t.m = b;
-    }
-    if (t.m == -INFINITY) continue;
-    const uint64_t minus_m = lm::pack2(-t.m, -t.m);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (j + u * kFwdThreads < nvec) {
-#pragma unroll
-        for (int i = 0; i < V::N / 2; ++i) {
-          uint64_t w = lm::mul2(lm::add2(V::pair(v[u], i), minus_m), c2);
-          float a, d;
-          lm::unpack2(w, a, d);
-          if (ENT) {
-            a = lm::max_nan(a, -200.f);
-            d = lm::max_nan(d, -200.f);
-            w = lm::pack2(a, d);
-          }
-          const uint64_t p = lm::pack2(lm::exp2_fast(a), lm::exp2_fast(d));
-          s2 = lm::add2(s2, p);
-          if (ENT) e2 = lm::fma2(p, w, e2);
-        }
-      }
-    }
+    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(xv + j + u * kFwdThreads);
+    add_vectors<T, ENT>(v, c, c2, own, r, s2, e2, nan);
+  }
+  for (; j < nvec; j += kFwdThreads) {
+    const uint4 v[1] = {__ldg(xv + j)};
+    add_vectors<T, ENT>(v, c, c2, own, r, s2, e2, nan);
   }
   {
-    float a, b;
-    lm::unpack2(s2, a, b);
-    t.s = a + b;
-    lm::unpack2(e2, a, b);
-    t.e = a + b;
+    float lo, hi;
+    lm::unpack2(s2, lo, hi);
+    s = lo + hi;
+    lm::unpack2(e2, lo, hi);
+    e = lo + hi;
   }
   // the entries before and after the vectors: fewer than 8 each
   {
@@ -304,17 +319,19 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
     if (at >= 0) {
       const float v = load_f32(x + at);
       nan |= !(v == v);
-      if (v > t.m) raise_max(t, v, c);
-      if (t.m != -INFINITY) {
-        const float w = lm::max_nan((v - t.m) * c, -200.f), p = lm::exp2_fast(w);
-        t.s += p;
-        t.e += p * w;
+      if (v > own) {
+        const float to = reference(v, c);
+        raise_to(s, e, r, to);
+        own = v;
+        r = to;
       }
+      const float w = lm::max_nan(fmaf(v, c, -r), -200.f), p = lm::exp2_fast(w);
+      s += p;
+      e += p * w;
     }
   }
-  if (nan) t.s = NAN;
-  // joint maximum, then the sums relative to it
-  float m = t.m;
+  // the slice's maximum, then the sums relative to it
+  float m = own;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) sh.warp_m[warp] = m;
@@ -322,28 +339,38 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
   m = sh.warp_m[0];
 #pragma unroll
   for (int w = 1; w < kFwdWarps; ++w) m = fmaxf(m, sh.warp_m[w]);
-  const float seen = nan ? NAN : t.m;
-  raise_max(t, m, c);
+  const float to = reference(m, c);
+  if (fabsf(m) != INFINITY && fabsf(m * c) == INFINITY) {
+    s = e = 0.f;
+    for (int32_t i = tid; i < n; i += kFwdThreads) {
+      const float w = lm::max_nan((load_f32(x + i) - m) * c, -200.f), p = lm::exp2_fast(w);
+      s += p;
+      e += p * w;
+    }
+  } else {
+    raise_to(s, e, r, to);
+  }
+  if (nan) s = NAN;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
-    if (ENT) t.e += __shfl_xor_sync(0xffffffffu, t.e, o);
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (ENT) e += __shfl_xor_sync(0xffffffffu, e, o);
   }
   if (lane == 0) {
-    sh.warp_s[warp] = t.s;
-    sh.warp_e[warp] = t.e;
+    sh.warp_s[warp] = s;
+    sh.warp_e[warp] = e;
   }
   __syncthreads();
   if (tid == 0) {
-    Sums r{m, 0.f, 0.f};
+    Sums t{m, to, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kFwdWarps; ++w) {
-      r.s += sh.warp_s[w];
-      r.e += sh.warp_e[w];
+      t.s += sh.warp_s[w];
+      t.e += sh.warp_e[w];
     }
-    sh.part = r;
+    sh.part = t;
   }
-  if (top_k > 0) slice_top<T>(sh, x, n, j0, head, nvec, seen, top_k);
+  if (top_k > 0) slice_top<T>(sh, x, n, j0, head, nvec, nan ? NAN : own, top_k);
 }
 
 // One cluster of CTAs per row (one CTA when the rows fill the GPU): every CTA
@@ -371,19 +398,27 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
   if (rank == 0) {
     if (threadIdx.x == 0) {
       Sums r = sh.part;
+      const float c = a.scale * kLog2e;
       if (parts > 1) {
         for (int p = 1; p < parts; ++p) r.m = fmaxf(r.m, cluster.map_shared_rank(&sh, p)->part.m);
-        const float m = r.m;
-        r.s = r.e = 0.f;
+        const float m = r.m, to = reference(m, c);
+        r = Sums{m, to, 0.f, 0.f};
+        const bool wide = fabsf(m) != INFINITY && fabsf(m * c) == INFINITY;
         for (int p = 0; p < parts; ++p) {
           Sums q = cluster.map_shared_rank(&sh, p)->part;
-          raise_max(q, m, a.scale * kLog2e);
+          if (wide) {
+            raise_to(q.s, q.e, (q.m - m) * c, 0.f);
+          } else {
+            raise_to(q.s, q.e, q.r, to);
+          }
           r.s += q.s;
           r.e += q.e;
         }
       }
       const bool empty = r.m == -INFINITY && r.s == 0.f;
-      const float log_sum = logf(r.s);
+      // the sums refer to r.r, the result to the maximum
+      const float off = fabsf(r.m * c) == INFINITY ? 0.f : -fmaf(r.m, c, -r.r);
+      const float log_sum = kLn2 * (log2f(r.s) + off);
       float lp = 0.f;
       if (tok >= a.vocab) {
         lp = NAN;
@@ -395,8 +430,8 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
       a.row_max[row] = r.m;
       a.log_sum[row] = log_sum;
       if (a.lse) a.lse[row] = empty ? -INFINITY : a.scale * r.m + log_sum;
-      if (ENT) a.entropy[row] = empty ? 0.f : log_sum - kLn2 * (r.e / r.s);
-      sh.part = Sums{r.m, log_sum, empty ? 1.f : 0.f};
+      if (ENT) a.entropy[row] = empty ? 0.f : kLn2 * (log2f(r.s) - r.e / r.s);
+      sh.part = Sums{r.m, log_sum, empty ? 1.f : 0.f, 0.f};
     }
     if (a.top_k > 0) {
       // the slices' keys: a key's rank among them is its place
@@ -412,10 +447,10 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
           for (int o = 0; o < num; ++o) at += all[o] > mine;
         }
         if (mine != 0 && at < a.top_k) {
-          const bool empty = sh.part.e != 0.f;
+          const bool empty = sh.part.s != 0.f;
           a.top_ids[row * a.top_k + at] = key_index(mine);
           a.top_logp[row * a.top_k + at] =
-              empty ? -INFINITY : a.scale * (key_value((uint32_t)(mine >> 32)) - sh.part.m) - sh.part.s;
+              empty ? -INFINITY : a.scale * (key_value((uint32_t)(mine >> 32)) - sh.part.m) - sh.part.r;
         }
       }
     }
