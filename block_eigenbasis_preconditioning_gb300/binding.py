@@ -30,6 +30,7 @@ FLAG_NONFINITE_G = 2
 FLAG_NONFINITE_A = 4
 FLAG_NOT_CONVERGED = 8
 FLAG_BAD_TOKEN = 16
+FLAG_TIMEOUT = 32
 
 # (name, restype, argtypes) of every exported symbol
 _c = ctypes

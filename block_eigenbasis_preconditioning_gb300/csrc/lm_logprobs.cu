@@ -12,6 +12,7 @@
 #include <cfloat>
 
 #include "lm_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace dobb {
 namespace {
@@ -57,8 +58,8 @@ struct LpGradArgs {
 // Where M c leaves the range of fp32 (masks of the type's lowest value and
 // nothing else in the row) the slice is summed again as 2^{(x - M) c}.
 //
-// The alternatives cost no second pass: the k-th largest of the 128 segments'
-// maxima (a segment: the entries of kThreads / 128 threads) is a lower bound
+// The alternatives cost no second pass: the k-th largest of the segments'
+// maxima (a segment: the entries of one thread) is a lower bound
 // of the k-th largest entry, so only segments whose maximum reaches it are
 // read again (about k of them, from L2), and their entries that reach it are
 // ranked by counting.  When more entries than the list holds reach the bound
@@ -67,10 +68,13 @@ struct LpGradArgs {
 constexpr int kFwdThreads = 256;
 constexpr int kFwdWarps = kFwdThreads / 32;
 constexpr int kUnroll = 4;
-constexpr int kSegs = 128;
-constexpr int kSegThreads = kFwdThreads / kSegs;
-constexpr int kCand = 256;
+constexpr int kSegs = kFwdThreads;
+constexpr int kPieces = 8;  // parts of a thread's entries that have a maximum of their own
+constexpr int kList = 128;
+constexpr int kHits = 64;
+constexpr int kCand = 128;
 constexpr int kMaxCluster = 8;
+constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Sums {
@@ -78,17 +82,30 @@ struct Sums {
   float s, e;  // e in units of log 2
 };
 
-struct FwdShared {
-  Sums part;       // of this CTA's slice of the row
-  unsigned long long best[DOBB_MAX_TOP_K];  // its largest keys, descending; 0 for none
-  float warp_m[kFwdWarps], warp_s[kFwdWarps], warp_e[kFwdWarps];
-  uint32_t seg[kSegs];
-  int32_t seg_list[kSegs];
-  uint32_t bound;
-  int32_t nseg, ncand;
+struct TopScratch {
+  unsigned long long best[DOBB_MAX_TOP_K];  // the largest keys, descending; 0 for none
   unsigned long long cand[kCand];
   unsigned long long warp_best[kFwdWarps];
+  uint32_t bound;
+  int32_t above, nlist, nhit, ncand;
+  int32_t list[2][kList];  // first vectors of the segments, and of their pieces, to be read again
+  int32_t hit_at[kHits];
+  uint4 hit[kHits];
 };
+
+struct FwdShared {
+  Sums part;  // of this CTA's slice of the row
+  float warp_m[kFwdWarps], warp_s[kFwdWarps], warp_e[kFwdWarps];
+  uint32_t seg[kSegs];  // key of every thread's maximum
+  TopScratch top;
+};
+
+// The upper half of a float that is not below x (NaN for NaN).
+__device__ __forceinline__ uint16_t upper_half(float x) {
+  if (!(x == x)) return 0x7fffu;
+  const uint32_t u = __float_as_uint(x);
+  return (uint16_t)((u + ((u & 0x80000000u) ? 0u : 0xffffu)) >> 16);
+}
 
 // Unsigned integers in the order of the floats; -0 equals 0, every NaN is
 // the largest.
@@ -121,105 +138,220 @@ __device__ __forceinline__ void raise_to(float& s, float& e, float from, float t
   s *= f;
 }
 
+__device__ __forceinline__ void order_desc(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+
 // The largest top_k keys of the slice x[0 .. n), which starts at index j0 of
-// the row, into sh.best; m is this thread's maximum (NaN if it saw one).
-template <typename T>
-__device__ void slice_top(FwdShared& sh, const T* x, int32_t n, int32_t j0, int32_t head, int32_t nvec,
-                          float m, int top_k) {
+// the row, into sh.best; seg: the key of every segment's maximum, visible to
+// all.  Segment s holds the vectors s, s + kSegs, ...; the first warp's lanes
+// hold the entries outside the vectors (sval at sat, sat < 0 for none).
+// pieces, if given: for every piece_vecs vectors of a segment (piece p of
+// segment s at p * kSegs + s) the upper half of a number that none of them
+// exceeds; then only the pieces that may hold something are read again.  Runs
+// on NW warps (the whole block, or one warp of it).
+template <typename T, int NW>
+__device__ __forceinline__ void slice_top(TopScratch& sh, const uint32_t* seg, const T* x, int32_t n,
+                                          int32_t j0, int32_t head, int32_t nvec, int32_t sat,
+                                          float sval, const uint16_t* pieces, int32_t piece_vecs,
+                                          int top_k) {
   using V = lm::Vec16<T>;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto sync = [] {
+    if (NW == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5, tid = warp * 32 + lane;
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  uint32_t k = order_key(m);
-#pragma unroll
-  for (int o = 1; o < kSegThreads; o <<= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-  if (tid % kSegThreads == 0) sh.seg[tid / kSegThreads] = k;
-  if (tid == 0) sh.ncand = 0;
-  __syncthreads();
   if (warp == 0) {
-    uint32_t s[kSegs / 32], keep[kSegs / 32];
+    constexpr int P = kSegs / 32;
+    static_assert(P == 8, "the sorting network below sorts 8 values");
+    uint32_t s[P], keep[P];
 #pragma unroll
-    for (int i = 0; i < kSegs / 32; ++i) keep[i] = s[i] = sh.seg[i * 32 + lane];
+    for (int i = 0; i < P; ++i) keep[i] = s[i] = seg[i * 32 + lane];
+    // every lane's values in descending order (Batcher's odd-even merge), then
+    // the largest of the lanes' first values is taken away top_k times
+#pragma unroll
+    for (int i = 0; i < P; i += 2) order_desc(s[i], s[i + 1]);
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+      order_desc(s[i], s[i + 2]);
+      order_desc(s[i + 1], s[i + 3]);
+      order_desc(s[i + 1], s[i + 2]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) order_desc(s[i], s[i + 4]);
+    order_desc(s[2], s[4]);
+    order_desc(s[3], s[5]);
+#pragma unroll
+    for (int i = 1; i < P - 1; i += 2) order_desc(s[i], s[i + 1]);
     uint32_t bound = kNegInfKey;
     for (int r = 0; r < top_k; ++r) {
-      uint32_t b = 0;
-#pragma unroll
-      for (int i = 0; i < kSegs / 32; ++i) b = max(b, s[i]);
-      bound = __reduce_max_sync(0xffffffffu, b);
+      bound = __reduce_max_sync(0xffffffffu, s[0]);
       if (bound <= kNegInfKey) break;
-      const unsigned who = __ballot_sync(0xffffffffu, b == bound);
+      const unsigned who = __ballot_sync(0xffffffffu, s[0] == bound);
       if (lane == __ffs(who) - 1) {
-        bool gone = false;
 #pragma unroll
-        for (int i = 0; i < kSegs / 32; ++i) {
-          if (!gone && s[i] == bound) {
-            s[i] = 0;
-            gone = true;
+        for (int i = 0; i < P - 1; ++i) s[i] = s[i + 1];
+        s[P - 1] = 0;
+      }
+    }
+    bound = max(bound, kNegInfKey);
+    // The entries that reach the bound are wanted.  Where it is -inf (fewer
+    // than top_k segments hold more), or where many segments' maxima equal it,
+    // those above it are, and then the first entries equal to it.
+    int reach = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) reach += __popc(__ballot_sync(0xffffffffu, keep[i] >= bound));
+    const bool above = bound == kNegInfKey || reach > top_k + 8;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const bool in = keep[i] > bound || (!above && keep[i] == bound);
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      // at most top_k + 8 segments: see `above`
+      if (in) sh.list[0][at + __popc(who & ((1u << lane) - 1u))] = i * 32 + lane;
+      at += __popc(who);
+    }
+    sh.best[lane] = 0;
+    if (lane == 0) {
+      sh.bound = bound;
+      sh.above = above;
+      sh.nlist = at;
+      sh.nhit = sh.ncand = 0;
+    }
+  }
+  sync();
+  const uint32_t bound = sh.bound;
+  const int32_t* list = sh.list[0];
+  int nlist = sh.nlist;
+  int32_t count = (nvec + kSegs - 1) / kSegs;  // vectors per entry of the list, kSegs apart
+  if (NW == 1 && pieces) {
+    const float low = key_value(bound);
+    const int np = (count + piece_vecs - 1) / piece_vecs;
+    int at = 0;
+    for (int i0 = 0; i0 < nlist * kPieces; i0 += 32) {
+      const int i = i0 + lane, p = i % kPieces;
+      int32_t first = 0;
+      bool in = i < nlist * kPieces && p < np;
+      if (in) {
+        const int32_t s = list[i / kPieces];
+        in = !(__uint_as_float((uint32_t)pieces[p * kSegs + s] << 16) < low);
+        first = s + p * piece_vecs * kSegs;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      const int mine = at + __popc(who & ((1u << lane) - 1u));
+      if (in && mine < kList) sh.list[1][mine] = first;
+      at += __popc(who);
+    }
+    if (at <= kList) {
+      list = sh.list[1];
+      nlist = at;
+      count = piece_vecs;
+    }
+    __syncwarp();
+  }
+  // Place of this lane among those of its warp that bring something.
+  auto place = [&](int* count, bool brings) {
+    const unsigned who = __ballot_sync(0xffffffffu, brings);
+    int first = 0;
+    if (who && lane == __ffs(who) - 1) first = atomicAdd(count, __popc(who));
+    return __shfl_sync(0xffffffffu, first, who ? __ffs(who) - 1 : 0) + __popc(who & ((1u << lane) - 1u));
+  };
+  // All entries whose key is at least `from`: first the vectors that hold one
+  // (2^span lanes take an entry of the list, kGroups loads in flight), then
+  // their entries.
+  auto collect = [&](uint32_t from) {
+    const float low = key_value(from);  // NaN where only NaN reaches `from`
+    constexpr int kGroups = NW == 1 ? 1 : 4;
+    const int span = count >= 32 ? 5 : 32 - __clz(count - 1), per = 32 >> span;
+    for (int32_t w0 = 0; w0 < count; w0 += 32) {
+      for (int q0 = warp * per; q0 < nlist; q0 += NW * kGroups * per) {
+        uint4 v[kGroups];
+        int32_t at[kGroups];
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          const int q = q0 + u * NW * per + (lane >> span);
+          const int32_t w = w0 + (lane & ((1 << span) - 1));
+          at[u] = q < nlist && w < count ? list[q] + w * kSegs : INT32_MAX;
+          if (at[u] < nvec) v[u] = __ldg(xv + at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          const uint4 one[1] = {v[u]};
+          const bool hit = at[u] < nvec && !(V::max_of(one) < low);
+          if (__any_sync(0xffffffffu, hit)) {
+            const int p = place(&sh.nhit, hit);
+            if (hit && p < kHits) {
+              sh.hit[p] = v[u];
+              sh.hit_at[p] = head + at[u] * V::N;
+            }
           }
         }
       }
     }
-    // fewer than top_k segments hold anything above -inf: everything above -inf counts
-    if (bound <= kNegInfKey) bound = kNegInfKey + 1;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kSegs / 32; ++i) {
-      const unsigned who = __ballot_sync(0xffffffffu, keep[i] >= bound);
-      if (keep[i] >= bound) sh.seg_list[at + __popc(who & ((1u << lane) - 1u))] = i * 32 + lane;
-      at += __popc(who);
+    sync();
+    const int hits = sh.nhit;
+    for (int i0 = warp * 32; i0 < min(hits, kHits) * V::N; i0 += 32 * NW) {
+      const int i = i0 + lane;
+      const bool in = i < min(hits, kHits) * V::N;
+      const float v = in ? load_f32(reinterpret_cast<const T*>(sh.hit) + i) : 0.f;
+      const bool brings = in && order_key(v) >= from;
+      const int p = place(&sh.ncand, brings);
+      if (brings && p < kCand) sh.cand[p] = full_key(v, j0 + sh.hit_at[i / V::N] + i % V::N);
     }
-    if (lane == 0) {
-      sh.bound = bound;
-      sh.nseg = at;
+    // the entries before and after the vectors
+    if (warp == 0) {
+      const bool brings = sat >= 0 && order_key(sval) >= from;
+      const int p = place(&sh.ncand, brings);
+      if (brings && p < kCand) sh.cand[p] = full_key(sval, j0 + sat);
     }
-  }
-  __syncthreads();
-  const uint32_t bound = sh.bound;
-  auto offer = [&](float v, int32_t j) {
-    if (order_key(v) >= bound) {
-      const int at = atomicAdd(&sh.ncand, 1);
-      if (at < kCand) sh.cand[at] = full_key(v, j0 + j);
-    }
+    sync();
+    const int found = hits > kHits ? kCand + 1 : sh.ncand;
+    sync();
+    if (tid == 0) sh.nhit = sh.ncand = 0;
+    sync();
+    return found;
   };
-  for (int q = warp; q < sh.nseg; q += kFwdWarps) {
-    const int first = sh.seg_list[q] * kSegThreads + lane % kSegThreads;
-    for (int32_t j = first + (lane / kSegThreads) * kFwdThreads; j < nvec;
-         j += (32 / kSegThreads) * kFwdThreads) {
-      const uint4 v[1] = {xv[j]};
-      if (order_key(V::max_of(v)) < bound) continue;
-#pragma unroll
-      for (int i = 0; i < V::N; ++i) offer(V::get(v[0], i), head + j * V::N + i);
-    }
+  bool above = sh.above;
+  int found = bound == 0xffffffffu && above ? 0 : collect(bound + (above ? 1 : 0));
+  if (found > kCand && !above) {  // many equal entries in few segments
+    above = true;
+    found = bound == 0xffffffffu ? 0 : collect(bound + 1);
   }
-  // the entries before and after the vectors
-  if (tid < head) offer(load_f32(x + tid), tid);
-  const int32_t tail0 = head + nvec * V::N;
-  if (tid >= 32 && tid - 32 < n - tail0) offer(load_f32(x + tail0 + tid - 32), tail0 + tid - 32);
-  if (tid < DOBB_MAX_TOP_K) sh.best[tid] = 0;
-  __syncthreads();
-  const int found = sh.ncand;
   if (found <= kCand) {
-    for (int i = tid; i < found; i += kFwdThreads) {
+    for (int i = tid; i < found; i += 32 * NW) {
       const unsigned long long mine = sh.cand[i];
       int rank = 0;
       for (int o = 0; o < found; ++o) rank += sh.cand[o] > mine;
       if (rank < top_k) sh.best[rank] = mine;
     }
-    // the rest of the answer is the first -inf entries
-    if (warp == 0 && found < top_k) {
+    if (above && warp == 0) {
       int at = found;
-      for (int32_t i = 0; i < n && at < top_k; i += 32) {
-        const bool is = i + lane < n && load_f32(x + i + lane) == -INFINITY;
-        const unsigned who = __ballot_sync(0xffffffffu, is);
-        const int mine = at + __popc(who & ((1u << lane) - 1u));
-        if (is && mine < top_k) sh.best[mine] = full_key(-INFINITY, j0 + i + lane);
-        at += __popc(who);
+      for (int32_t i = 0; i < n && at < top_k; i += 128) {
+        float v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = i + u * 32 + lane < n ? load_f32(x + i + u * 32 + lane) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const bool is = i + u * 32 + lane < n && order_key(v[u]) == bound;
+          const unsigned who = __ballot_sync(0xffffffffu, is);
+          const int mine = at + __popc(who & ((1u << lane) - 1u));
+          if (is && mine < top_k) sh.best[mine] = full_key(v[u], j0 + i + u * 32 + lane);
+          at += __popc(who);
+        }
       }
     }
   } else {
+    // hundreds of different entries above the bound within fewer than top_k
+    // segments: the largest key below the last one, top_k times
     unsigned long long last = ~0ull;
     for (int r = 0; r < top_k; ++r) {
       unsigned long long b = 0;
-      for (int32_t j = tid; j < n; j += kFwdThreads) {
+      for (int32_t j = tid; j < n; j += 32 * NW) {
         const unsigned long long key = full_key(load_f32(x + j), j0 + j);
         if (key < last && key > b) b = key;
       }
@@ -228,25 +360,28 @@ __device__ void slice_top(FwdShared& sh, const T* x, int32_t n, int32_t j0, int3
         const unsigned long long c = __shfl_xor_sync(0xffffffffu, b, o);
         b = c > b ? c : b;
       }
-      if (lane == 0) sh.warp_best[warp] = b;
-      __syncthreads();
-      b = sh.warp_best[0];
-      for (int w = 1; w < kFwdWarps; ++w) b = sh.warp_best[w] > b ? sh.warp_best[w] : b;
+      if (NW > 1) {
+        if (lane == 0) sh.warp_best[warp] = b;
+        __syncthreads();
+        b = sh.warp_best[0];
+        for (int w = 1; w < NW; ++w) b = sh.warp_best[w] > b ? sh.warp_best[w] : b;
+      }
       last = b;
       if (tid == 0) sh.best[r] = b;
-      __syncthreads();
+      sync();
     }
   }
-  __syncthreads();
+  sync();
 }
 
 // The vectors v of a thread onto its maximum and sums (s2, e2: two sums each,
-// for the even and the odd entries)
+// for the even and the odd entries); returns their largest value, NaN for NaN
 template <typename T, bool ENT, int U>
-__device__ __forceinline__ void add_vectors(const uint4 (&v)[U], float c, uint64_t c2, float& m, float& r,
-                                            uint64_t& s2, uint64_t& e2, bool& nan) {
+__device__ __forceinline__ float add_vectors(const uint4 (&v)[U], float c, uint64_t c2, float& m,
+                                             float& r, uint64_t& s2, uint64_t& e2, bool& nan) {
   using V = lm::Vec16<T>;
-  float b = V::max_of(v);
+  const float largest = V::max_of(v);
+  float b = largest;
   if (!(b == b)) {  // the maximum of the others
     nan = true;
     b = -INFINITY;
@@ -281,6 +416,7 @@ __device__ __forceinline__ void add_vectors(const uint4 (&v)[U], float c, uint64
       if (ENT) e2 = lm::fma2(p, w, e2);
     }
   }
+  return largest;
 }
 
 // Maximum, sums and the largest keys of one slice, into sh.part and sh.best
@@ -313,22 +449,21 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
     e = lo + hi;
   }
   // the entries before and after the vectors: fewer than 8 each
-  {
-    const int32_t tail0 = head + nvec * V::N;
-    const int32_t at = tid < head ? tid : (tid >= 32 && tid - 32 < n - tail0) ? tail0 + tid - 32 : -1;
-    if (at >= 0) {
-      const float v = load_f32(x + at);
-      nan |= !(v == v);
-      if (v > own) {
-        const float to = reference(v, c);
-        raise_to(s, e, r, to);
-        own = v;
-        r = to;
-      }
-      const float w = lm::max_nan(fmaf(v, c, -r), -200.f), p = lm::exp2_fast(w);
-      s += p;
-      e += p * w;
+  const int32_t tail0 = head + nvec * V::N;
+  const int32_t sat = tid < head ? tid : (tid >= 16 && tid - 16 < n - tail0) ? tail0 + tid - 16 : -1;
+  float sval = -INFINITY;
+  if (sat >= 0) {
+    sval = load_f32(x + sat);
+    nan |= !(sval == sval);
+    if (sval > own) {
+      const float to = reference(sval, c);
+      raise_to(s, e, r, to);
+      own = sval;
+      r = to;
     }
+    const float w = lm::max_nan(fmaf(sval, c, -r), -200.f), p = lm::exp2_fast(w);
+    s += p;
+    e += p * w;
   }
   // the slice's maximum, then the sums relative to it
   float m = own;
@@ -370,7 +505,35 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
     }
     sh.part = t;
   }
-  if (top_k > 0) slice_top<T>(sh, x, n, j0, head, nvec, nan ? NAN : own, top_k);
+  if (top_k > 0) {
+    sh.seg[tid] = order_key(nan ? NAN : own);
+    __syncthreads();
+    slice_top<T, kFwdWarps>(sh.top, sh.seg, x, n, j0, head, nvec, sat, sval, nullptr, 0, top_k);
+  }
+}
+
+// The row's results but the alternatives; returns log_sum.
+template <bool ENT>
+__device__ __forceinline__ float write_row(const LpArgs& a, int64_t row, const Sums& r, int64_t tok,
+                                           float given) {
+  const float c = a.scale * kLog2e;
+  const bool empty = r.m == -INFINITY && r.s == 0.f;
+  // the sums refer to r.r, the result to the maximum
+  const float off = fabsf(r.m * c) == INFINITY ? 0.f : -fmaf(r.m, c, -r.r);
+  const float log_sum = kLn2 * (log2f(r.s) + off);
+  float lp = 0.f;
+  if (tok >= a.vocab) {
+    lp = NAN;
+    if (a.flags) atomicOr(a.flags, DOBB_FLAG_BAD_TOKEN);
+  } else if (tok >= 0) {
+    lp = empty ? -INFINITY : a.scale * (given - r.m) - log_sum;
+  }
+  a.logp[row] = lp;
+  a.row_max[row] = r.m;
+  a.log_sum[row] = log_sum;
+  if (a.lse) a.lse[row] = empty ? -INFINITY : a.scale * r.m + log_sum;
+  if (ENT) a.entropy[row] = empty ? 0.f : kLn2 * (log2f(r.s) - r.e / r.s);
+  return log_sum;
 }
 
 // One cluster of CTAs per row (one CTA when the rows fill the GPU): every CTA
@@ -415,29 +578,15 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
           r.e += q.e;
         }
       }
+      const float log_sum = write_row<ENT>(a, row, r, tok, given);
       const bool empty = r.m == -INFINITY && r.s == 0.f;
-      // the sums refer to r.r, the result to the maximum
-      const float off = fabsf(r.m * c) == INFINITY ? 0.f : -fmaf(r.m, c, -r.r);
-      const float log_sum = kLn2 * (log2f(r.s) + off);
-      float lp = 0.f;
-      if (tok >= a.vocab) {
-        lp = NAN;
-        if (a.flags) atomicOr(a.flags, DOBB_FLAG_BAD_TOKEN);
-      } else if (tok >= 0) {
-        lp = empty ? -INFINITY : a.scale * (given - r.m) - log_sum;
-      }
-      a.logp[row] = lp;
-      a.row_max[row] = r.m;
-      a.log_sum[row] = log_sum;
-      if (a.lse) a.lse[row] = empty ? -INFINITY : a.scale * r.m + log_sum;
-      if (ENT) a.entropy[row] = empty ? 0.f : kLn2 * (log2f(r.s) - r.e / r.s);
       sh.part = Sums{r.m, log_sum, empty ? 1.f : 0.f, 0.f};
     }
     if (a.top_k > 0) {
       // the slices' keys: a key's rank among them is its place
       const int num = parts * a.top_k;
       for (int i = threadIdx.x; i < num; i += kFwdThreads)
-        all[i] = parts > 1 ? cluster.map_shared_rank(&sh, i / a.top_k)->best[i % a.top_k] : sh.best[i];
+        all[i] = parts > 1 ? cluster.map_shared_rank(&sh, i / a.top_k)->top.best[i % a.top_k] : sh.top.best[i];
       __syncthreads();
       for (int i = threadIdx.x; i < num; i += kFwdThreads) {
         const unsigned long long mine = all[i];
@@ -456,6 +605,208 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
     }
   }
   if (parts > 1) cluster.sync();  // the slices' shared memory stays until it was read
+}
+
+// ------------------------------------------------ forward, many long rows
+//
+// Persistent blocks take the rows in turn.  One thread streams them through a
+// ring of shared memory with bulk copies, so that the next rows are on their
+// way whatever the other warps do; eight warps keep the maxima and sums, each
+// at its own pace; two more warps, row about, join them, find the alternatives
+// and write the row while the eight are in the next ones.
+constexpr int kStageVecs = kUnroll * kFwdThreads;
+constexpr int kStages = 3;
+constexpr int kJoinWarps = 3;  // take the rows in turn
+constexpr int kRingThreads = kFwdThreads + 32 + 32 * kJoinWarps;
+constexpr int kRingBlocks = 3;  // per SM
+
+struct RingShared {
+  uint64_t full[kStages], empty[kStages], row_full[kJoinWarps], row_empty[kJoinWarps];
+  int32_t abort;
+  Sums stat[kJoinWarps][kFwdWarps];
+  uint32_t seg[kJoinWarps][kSegs];  // key of every thread's maximum
+  uint16_t pieces[kJoinWarps][kPieces * kSegs];
+  TopScratch top[kJoinWarps];
+};
+
+// Wait for a phase; false once a wait of this block has run out of time.
+__device__ __forceinline__ bool ring_wait(RingShared& sh, uint64_t* bar, uint32_t parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (*(volatile int32_t*)&sh.abort) return false;
+    if (ptx::global_timer_ns() - t0 > 2000000000ull) {
+      *(volatile int32_t*)&sh.abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(const LpArgs a, int64_t rows) {
+  using V = lm::Vec16<T>;
+  extern __shared__ __align__(128) unsigned char raw[];
+  uint4* ring = reinterpret_cast<uint4*>(raw);
+  RingShared& sh = *reinterpret_cast<RingShared*>(raw + (size_t)kStages * kStageVecs * 16);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sh.full[s], 1);
+      ptx::mbar_init(&sh.empty[s], kFwdWarps);
+    }
+    for (int s = 0; s < kJoinWarps; ++s) {
+      ptx::mbar_init(&sh.row_full[s], kFwdWarps);
+      ptx::mbar_init(&sh.row_empty[s], 1);
+    }
+    sh.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const T* logits = static_cast<const T*>(a.logits);
+  const float c = a.scale * kLog2e;
+  uint32_t it = 0;  // stages so far
+  if (warp > kJoinWarps) {
+    const int mtid = tid - 32 * (kJoinWarps + 1), mwarp = warp - kJoinWarps - 1;
+    const uint64_t c2 = lm::pack2(c, c);
+    uint32_t i = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, ++i) {
+      const T* x = logits + row * a.row_stride;
+      const int32_t head = (int32_t)lm::head_of(x, a.vocab), nvec = (a.vocab - head) / V::N;
+      float own = -INFINITY, r = -FLT_MAX, piece = -INFINITY;
+      bool nan = false;
+      uint64_t s2 = 0, e2 = 0;
+      const uint32_t buf = i % kJoinWarps;
+      const int fold = nvec / kStageVecs / kPieces + 1;  // stages per piece
+      int left = fold;
+      uint16_t* pieces = sh.pieces[buf] + mtid;
+      if (i >= kJoinWarps && !ring_wait(sh, &sh.row_empty[buf], ((i / kJoinWarps) & 1) ^ 1)) return;
+      for (int32_t v0 = 0; v0 < nvec; v0 += kStageVecs, ++it) {
+        const uint32_t st = it % kStages;
+        if (!ring_wait(sh, &sh.full[st], (it / kStages) & 1)) return;
+        const uint4* src = ring + st * kStageVecs + mtid;
+        if (nvec - v0 >= kStageVecs) {
+          uint4 v[kUnroll];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) v[u] = src[u * kFwdThreads];
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.empty[st]);
+          piece = lm::max_nan(piece, add_vectors<T, ENT>(v, c, c2, own, r, s2, e2, nan));
+        } else {
+          for (int32_t j = v0 + mtid; j < nvec; j += kFwdThreads) {
+            const uint4 v[1] = {src[j - v0 - mtid]};
+            piece = lm::max_nan(piece, add_vectors<T, ENT>(v, c, c2, own, r, s2, e2, nan));
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.empty[st]);
+        }
+        if (a.top_k > 0 && (--left == 0 || v0 + kStageVecs >= nvec)) {
+          *pieces = upper_half(piece);
+          pieces += kSegs;
+          piece = -INFINITY;
+          left = fold;
+        }
+      }
+      float m = own, s, e, hi;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      lm::unpack2(s2, s, hi);
+      s += hi;
+      lm::unpack2(e2, e, hi);
+      e += hi;
+      const float to = reference(m, c);
+      raise_to(s, e, r, to);
+      if (nan) s = NAN;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (ENT) e += __shfl_xor_sync(0xffffffffu, e, o);
+      }
+      if (a.top_k > 0) sh.seg[buf][mtid] = order_key(nan ? NAN : own);
+      if (lane == 0) sh.stat[buf][mwarp] = Sums{m, to, s, e};
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.row_full[buf]);
+    }
+  } else if (warp == kJoinWarps) {
+    if (lane != 0) return;
+    bool ok = true;
+    for (int64_t row = blockIdx.x; row < rows && ok; row += gridDim.x) {
+      const T* x = logits + row * a.row_stride;
+      const int32_t head = (int32_t)lm::head_of(x, a.vocab), nvec = (a.vocab - head) / V::N;
+      const uint4* src = reinterpret_cast<const uint4*>(x + head);
+      for (int32_t v0 = 0; v0 < nvec; v0 += kStageVecs, ++it) {
+        const uint32_t st = it % kStages;
+        if (it >= kStages && !(ok = ring_wait(sh, &sh.empty[st], ((it / kStages) & 1) ^ 1))) break;
+        const uint32_t bytes = (uint32_t)min(nvec - v0, kStageVecs) * 16;
+        ptx::mbar_arrive_expect_tx(&sh.full[st], bytes);
+        ptx::bulk_load(ring + st * kStageVecs, src + v0, bytes, &sh.full[st]);
+      }
+    }
+    // no copy is in flight when the block ends, whatever ended the rows
+    for (uint32_t p = it > kStages ? it - kStages : 0; p < it; ++p)
+      ptx::mbar_wait(&sh.full[p % kStages], (p / kStages) & 1);
+  } else {
+    const int buf = warp;
+    TopScratch& top = sh.top[buf];
+    uint32_t i = 0;
+    for (int64_t row = blockIdx.x + (int64_t)buf * gridDim.x; row < rows; row += (int64_t)kJoinWarps * gridDim.x, ++i) {
+      const T* x = logits + row * a.row_stride;
+      const int32_t head = (int32_t)lm::head_of(x, a.vocab), nvec = (a.vocab - head) / V::N;
+      const int32_t tail0 = head + nvec * V::N;
+      // the given token's logit, and the entries before and after the vectors
+      const int64_t tok = lm::load_token(a.tokens, a.token_bytes, row);
+      const float given = tok >= 0 && tok < a.vocab ? load_f32(x + tok) : 0.f;
+      const int32_t at = lane < head ? lane : (lane >= 16 && lane - 16 < a.vocab - tail0) ? tail0 + lane - 16 : -1;
+      const float single = at >= 0 ? load_f32(x + at) : -INFINITY;
+      if (!ring_wait(sh, &sh.row_full[buf], i & 1)) {
+        if (lane == 0 && a.flags) atomicOr(a.flags, DOBB_FLAG_TIMEOUT);
+        return;
+      }
+      Sums t{-INFINITY, -FLT_MAX, 0.f, 0.f};
+      if (lane < kFwdWarps) t = sh.stat[buf][lane];
+      const float m1 = fmaxf(t.m, single);
+      float m = m1;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float to = reference(m, c);
+      if (fabsf(m) != INFINITY && fabsf(m * c) == INFINITY) {
+        t.s = t.e = 0.f;
+        for (int32_t j = lane; j < a.vocab; j += 32) {
+          const float w = lm::max_nan((load_f32(x + j) - m) * c, -200.f), p = lm::exp2_fast(w);
+          t.s += p;
+          t.e += p * w;
+        }
+      } else {
+        raise_to(t.s, t.e, t.r, to);
+        const float w = lm::max_nan(fmaf(single, c, -to), -200.f), p = lm::exp2_fast(w);
+        t.s += p;
+        t.e += p * w;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+        if (ENT) t.e += __shfl_xor_sync(0xffffffffu, t.e, o);
+      }
+      t.m = m;
+      t.r = to;
+      float log_sum = 0.f;
+      if (lane == 0) log_sum = write_row<ENT>(a, row, t, tok, given);
+      if (a.top_k > 0) {
+        log_sum = __shfl_sync(0xffffffffu, log_sum, 0);
+        const bool empty = m == -INFINITY && t.s == 0.f;
+        slice_top<T, 1>(top, sh.seg[buf], x, a.vocab, 0, head, nvec, at, single, sh.pieces[buf],
+                        (nvec / kStageVecs / kPieces + 1) * kUnroll, a.top_k);
+        if (lane < a.top_k) {
+          const unsigned long long key = top.best[lane];
+          a.top_ids[row * a.top_k + lane] = key_index(key);
+          a.top_logp[row * a.top_k + lane] =
+              empty ? -INFINITY : a.scale * (key_value((uint32_t)(key >> 32)) - m) - log_sum;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.row_empty[buf]);
+    }
+  }
 }
 
 // --------------------------------------------------------------- gradient
@@ -586,8 +937,26 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
   if (top_k > 0 && (!top_ids || !top_logp))
     return fail(DOBB_ERR_INVALID_ARG, "top_ids and top_logp must be non-NULL when top_k > 0");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows >= 2 * kSms && vocab * (int64_t)lm::dtype_bytes(logits_dtype) >= 32768 && vocab <= (1 << 20)) {
+    const LpArgs a{logits, row_stride, (int32_t)vocab, tokens,  token_bytes, scale,    top_k, logp,
+                   lse,    row_max,    log_sum,        entropy, top_ids,     top_logp, flags};
+    const size_t smem = (size_t)kStages * kStageVecs * 16 + sizeof(RingShared);
+    const unsigned grid = (unsigned)(rows < kSms * kRingBlocks ? rows : kSms * kRingBlocks);
+    auto launch = [&](auto kernel) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      kernel<<<grid, kRingThreads, smem, s>>>(a, rows);
+      return cudaGetLastError();
+    };
+    cudaError_t e = logits_dtype == DOBB_F32
+                        ? (entropy ? launch(lp_forward_ring<float, true>) : launch(lp_forward_ring<float, false>))
+                        : (entropy ? launch(lp_forward_ring<__nv_bfloat16, true>)
+                                   : launch(lp_forward_ring<__nv_bfloat16, false>));
+    if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "log-probability launch: %s", cudaGetErrorString(e));
+    return DOBB_OK;
+  }
   int parts = 1;
-  while (parts < kMaxCluster && rows * parts < 152 && vocab / parts > 4096) parts *= 2;
+  while (parts < kMaxCluster && rows * parts < kSms && vocab / parts > 4096) parts *= 2;
   // a launch holds up to 2^31 - 1 blocks
   const int64_t most = ((int64_t)1 << 30) / parts;
   cudaError_t e = cudaSuccess;

@@ -356,6 +356,7 @@ const char* dobb_eigh_noalloc_last_error(void);
  * Token indices are int32 or int64 (token_bytes 4 or 8).  `flags_dev` is an
  * optional device uint32 that condition bits are OR-ed into. */
 #define DOBB_FLAG_BAD_TOKEN 16u /* a token index >= vocab                       */
+#define DOBB_FLAG_TIMEOUT 32u   /* a device-side wait gave up: the call's results are not valid */
 
 /* Largest number of alternatives dobb_log_probs returns per row. */
 #define DOBB_MAX_TOP_K 32

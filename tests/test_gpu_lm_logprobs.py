@@ -90,6 +90,26 @@ def test_alternatives_with_many_ties(dtype, k, vocab):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [1, 9, 32])
+def test_alternatives_with_many_ties_over_many_long_rows(dtype, k):
+    rng = np.random.default_rng(k)
+    rows, vocab = 310, 17003
+    x = rng.integers(-2, 3, (rows, vocab)).astype(np.float32)
+    x[1::4] = 0.0
+    x[2::4] = -np.inf
+    x[2::8, 5::1000] = 1.0                # 17 tokens are possible
+    x[3::4] = rounded(rng.standard_normal((len(x[3::4]), vocab)), dtype)
+    x[3::8, 77::256 * 8] += 8.0           # the largest sit far apart in one stride
+    x[3::8] = rounded(x[3::8], dtype)
+    x[7::16, :600] = 9.0 + np.arange(600) # and one next to the other
+    x[7::16] = rounded(x[7::16], dtype)
+    x[0] = np.sort(x[0])
+    t = rng.integers(0, vocab, rows)
+    _, _, r = _forward(x, t, dtype, 1.0, k, 3, 1)
+    _check_forward(x, t, r, 1.0, k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows", [1, 6, 400])
 @pytest.mark.parametrize("vocab", [37, 4000, 40001])
 def test_masked_rows_lowest_values_and_non_finite(dtype, rows, vocab):
