@@ -1,34 +1,55 @@
-// Global l2 norm of a set of gradients, and clipping by it.
+// Global l2 norm of a set of gradients, and clipping by it, in two kernels.
 //
-// The entries are cut into chunks; a chunk's sum of squares is a double in
-// the workspace.  The chunks of a tensor, and then the tensors, are summed in
-// a fixed order.
+// The tensors' entries are cut into chunks, and the chunks, tensor after
+// tensor, into one stretch of equal length per CTA.  The first kernel squares
+// and sums: a CTA leaves one fp64 sum per tensor of its stretch, in slot (CTA +
+// tensor), which no other pair has, and zeros in the slots between its own
+// and the next CTA's.  The second kernel sums the slots (every CTA all of
+// them, in the same order: some KB from L2), and scales the stretches, last
+// chunk first: what the first kernel read last is still in L2.
+//
+// Within a chunk a thread sums the squares of its 32 entries in four fp32
+// chains, and adds the result to an fp32 pair (hi, lo) that loses nothing.
+// Where the sum leaves the range in which fp32 squares are exact enough (large,
+// tiny or non-finite entries), the thread sums its entries again in fp64.
 #include "lm_common.cuh"
 
 namespace dobb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 32768;          // entries per chunk
-constexpr int kTensorsPerLaunch = 512; // pointer tables travel in the kernel parameters
+constexpr int kChunk = 8192;  // entries
+constexpr int kSms = 152;
+constexpr int kMaxTensors = 512;  // of a launch: the tables travel in the kernel parameters
+constexpr int kFewTensors = 32;   // a table of 1 KB, launched faster
 
-struct ClipArgs {
-  int32_t num;             // tensors of this launch
-  int64_t chunk_base;      // chunks of the launches before
-  double* chunk_sums;      // one per chunk
-  double* tensor_sums;     // one per tensor of this launch
-  const float* stats;      // [1] = c
-  const void* g[kTensorsPerLaunch];
-  void* out[kTensorsPerLaunch];
-  int64_t numel[kTensorsPerLaunch];
-  int32_t chunk0[kTensorsPerLaunch + 1];  // first chunk of every tensor, within this launch
-  uint8_t g_bf16[kTensorsPerLaunch], out_bf16[kTensorsPerLaunch];
+template <int K>
+struct Table {
+  int32_t num;        // tensors
+  int32_t chunks, grid;
+  int64_t slot0;      // first slot of this launch
+  const void* g[K];
+  void* out[K];
+  int64_t numel[K];
+  int32_t chunk0[K + 1];  // first chunk of every tensor
+  uint8_t g_bf16[K], out_bf16[K];
 };
 
 int64_t chunks_of(int64_t numel) { return (numel + kChunk - 1) / kChunk; }
 
+// Stretch of CTA b: chunks [first(b), first(b + 1)); the CTA of chunk c.
+template <int K>
+__device__ __forceinline__ int32_t first_chunk(const Table<K>& a, int32_t b) {
+  return (int32_t)((int64_t)b * a.chunks / a.grid);
+}
+template <int K>
+__device__ __forceinline__ int32_t cta_of(const Table<K>& a, int32_t c) {
+  return (int32_t)((((int64_t)c + 1) * a.grid - 1) / a.chunks);
+}
+
 // the tensor that chunk c belongs to
-__device__ __forceinline__ int tensor_of(const ClipArgs& a, int32_t c) {
+template <int K>
+__device__ __forceinline__ int tensor_of(const Table<K>& a, int32_t c) {
   int lo = 0, hi = a.num;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -40,90 +61,310 @@ __device__ __forceinline__ int tensor_of(const ClipArgs& a, int32_t c) {
   return lo;
 }
 
-__device__ __forceinline__ float load_any(const void* p, bool bf16, int64_t i) {
-  return bf16 ? load_f32(static_cast<const __nv_bfloat16*>(p) + i)
-              : load_f32(static_cast<const float*>(p) + i);
-}
-
-__global__ void __launch_bounds__(kThreads) clip_chunk_sums(const __grid_constant__ ClipArgs a) {
-  __shared__ double red[32];
-  for (int32_t c = blockIdx.x; c < a.chunk0[a.num]; c += gridDim.x) {
-    const int t = tensor_of(a, c);
-    const int64_t lo = (int64_t)(c - a.chunk0[t]) * kChunk, hi = min(a.numel[t], lo + kChunk);
-    double s = 0.0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-      const double v = load_any(a.g[t], a.g_bf16[t], i);
-      s += v * v;
-    }
-    s = block_sum_d(s, red);
-    if (threadIdx.x == 0) a.chunk_sums[a.chunk_base + c] = s;
+// A thread's sum of squares: hi + lo + wide.
+struct Squares {
+  float hi = 0.f, lo = 0.f;
+  double wide = 0.0;
+  __device__ __forceinline__ void add(float s) {  // Knuth's two-sum
+    const float t = hi + s, z = t - hi;
+    lo += (hi - (t - z)) + (s - z);
+    hi = t;
   }
-}
-
-__global__ void __launch_bounds__(kThreads) clip_tensor_sums(const __grid_constant__ ClipArgs a) {
-  __shared__ double red[32];
-  for (int t = blockIdx.x; t < a.num; t += gridDim.x) {
-    double s = 0.0;
-    for (int32_t c = a.chunk0[t] + threadIdx.x; c < a.chunk0[t + 1]; c += kThreads)
-      s += a.chunk_sums[a.chunk_base + c];
-    s = block_sum_d(s, red);
-    if (threadIdx.x == 0) a.tensor_sums[t] = s;
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) clip_finish(const double* tensor_sums, int num,
-                                                        float max_norm, float* stats,
-                                                        uint32_t* flags) {
-  __shared__ double red[32];
-  double s = 0.0;
-  for (int t = threadIdx.x; t < num; t += kThreads) {
-    s += tensor_sums[t];
-    stats[2 + t] = (float)sqrt(tensor_sums[t]);
-  }
-  s = block_sum_d(s, red);
-  if (threadIdx.x == 0) {
-    const double norm = sqrt(s);
-    const bool finite = isfinite(norm);
-    stats[0] = (float)norm;
-    stats[1] = (finite && norm > (double)max_norm) ? (float)((double)max_norm / norm) : 1.f;
-    if (!finite && flags) atomicOr(flags, DOBB_FLAG_NONFINITE_G);
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) clip_scale(const __grid_constant__ ClipArgs a) {
-  const float f = a.stats[1];
-  for (int32_t c = blockIdx.x; c < a.chunk0[a.num]; c += gridDim.x) {
-    const int t = tensor_of(a, c);
-    if (f == 1.f && a.out[t] == a.g[t] && a.g_bf16[t] == a.out_bf16[t]) continue;
-    const int64_t lo = (int64_t)(c - a.chunk0[t]) * kChunk, hi = min(a.numel[t], lo + kChunk);
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-      const float v = f * load_any(a.g[t], a.g_bf16[t], i);
-      if (a.out_bf16[t])
-        store_f32(static_cast<__nv_bfloat16*>(a.out[t]) + i, v);
-      else
-        store_f32(static_cast<float*>(a.out[t]) + i, v);
-    }
-  }
-}
-
-struct Workspace {
-  int64_t chunks;
-  size_t tensor_off, total;
 };
 
-dobb_status measure(int num, const int64_t* numel, Workspace* w) {
+// Where 32 squares sum to less than this, their rounding (2^-150 each, below
+// the smallest normal number) could show; zeros alone are exact.
+constexpr float kSmallest = 1.2e-35f;  // 2^-116
+
+template <typename T>
+__device__ __forceinline__ void add_chunk(Squares& sum, const T* p, int32_t n) {
+  using V = lm::Vec16<T>;
+  constexpr int kVecs = kChunk / V::N / kThreads;
+  const int32_t head = (int32_t)lm::head_of(p, n), nvec = (n - head) / V::N, tail0 = head + nvec * V::N;
+  const uint4* v = reinterpret_cast<const uint4*>(p + head);
+  const int tid = threadIdx.x;
+  // an entry before or behind the vectors: fewer than 8 each
+  const int32_t at = tid < head ? tid : (tid >= 32 && tid - 32 < n - tail0) ? tail0 + tid - 32 : -1;
+  uint4 x[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u)
+    x[u] = tid + u * kThreads < nvec ? __ldg(v + tid + u * kThreads) : make_uint4(0, 0, 0, 0);
+  const float single = at >= 0 ? load_f32(p + at) : 0.f;
+  uint64_t s[2] = {0, 0};
+  uint32_t bits = 0;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    bits |= x[u].x | x[u].y | x[u].z | x[u].w;
+#pragma unroll
+    for (int i = 0; i < V::N / 2; ++i) {
+      const uint64_t w = V::pair(x[u], i);
+      s[i & 1] = lm::fma2(w, w, s[i & 1]);
+    }
+  }
+  float a, b, c, d;
+  lm::unpack2(s[0], a, b);
+  lm::unpack2(s[1], c, d);
+  const float t = fmaf(single, single, (a + b) + (c + d));
+  // (bits: the signs of zeros are no entries)
+  const bool zero = (bits & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) == 0 && single == 0.f;
+  if ((t >= kSmallest && t < INFINITY) || zero) {
+    sum.add(t);
+  } else {
+#pragma unroll 1
+    for (int32_t j = tid; j < nvec; j += kThreads)
+#pragma unroll 1
+      for (int i = 0; i < V::N; ++i) {
+        const double y = load_f32(p + head + j * V::N + i);
+        sum.wide += y * y;
+      }
+    sum.wide += (double)single * single;
+  }
+}
+
+template <int K>
+__global__ void __launch_bounds__(kThreads, 4) clip_sums(const __grid_constant__ Table<K> a, double* slots) {
+  __shared__ double red[32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  slots += a.slot0;
+  const int32_t b = blockIdx.x, end = first_chunk(a, b + 1);
+  int32_t c = first_chunk(a, b);
+  int t = tensor_of(a, c);
+  if (b == 0)
+    for (int i = threadIdx.x; i < t; i += kThreads) slots[i] = 0.0;
+  while (c < end) {
+    Squares sum;
+    const int32_t stop = min(end, a.chunk0[t + 1]);
+    for (; c < stop; ++c) {
+      const int64_t lo = (int64_t)(c - a.chunk0[t]) * kChunk;
+      const int32_t n = (int32_t)min((int64_t)kChunk, a.numel[t] - lo);
+      if (a.g_bf16[t])
+        add_chunk(sum, static_cast<const __nv_bfloat16*>(a.g[t]) + lo, n);
+      else
+        add_chunk(sum, static_cast<const float*>(a.g[t]) + lo, n);
+    }
+    const double s = block_sum_d((double)sum.hi + sum.lo + sum.wide, red);
+    // the next slot that is written by this CTA or the next one
+    int next = t;
+    int32_t after = a.grid + a.num;
+    if (c < a.chunks) {
+      do ++next;
+      while (next < a.num && a.chunk0[next + 1] <= c);
+      if (c < a.chunk0[t + 1]) next = t;
+      after = b + (c == end) + next;
+    }
+    if (threadIdx.x == 0) slots[b + t] = s;
+    for (int i = b + t + 1 + threadIdx.x; i < after; i += kThreads) slots[i] = 0.0;
+    t = next;
+  }
+}
+
+// Four entries (eight where both sides are bf16), a whole number of loads and
+// stores of up to 16 bytes, neighbouring lanes side by side.
+template <typename T, int E>
+struct Entries {
+  static constexpr int kWords = E * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if (kWords == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x, w[1] = v.y, w[kWords - 2] = v.z, w[kWords - 1] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if (kWords == 4)
+      __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[kWords - 2], w[kWords - 1]));
+    else
+      __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    return sizeof(T) == 2 ? lm::pack2(lm::bf16_lo(w[i]), lm::bf16_hi(w[i]))
+                          : lm::pack2(__uint_as_float(w[2 * i % kWords]), __uint_as_float(w[(2 * i + 1) % kWords]));
+  }
+  __device__ __forceinline__ void put(int i, uint64_t v) {
+    float lo, hi;
+    lm::unpack2(v, lo, hi);
+    if (sizeof(T) == 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      w[2 * i % kWords] = __float_as_uint(lo);
+      w[(2 * i + 1) % kWords] = __float_as_uint(hi);
+    }
+  }
+};
+
+// Input and output misaligned against each other (or at an end of a tensor).
+// Out of line: it would only push the common path out of the instruction cache.
+template <typename G, typename O>
+__device__ __noinline__ void scale_any(const G* p, O* o, int32_t n, float f) {
+#pragma unroll 8
+  for (int32_t j = threadIdx.x; j < n; j += kThreads) store_f32(o + j, f * load_f32(p + j));
+}
+
+template <typename G, typename O>
+__device__ __forceinline__ void scale_chunk(const G* p, O* o, int32_t n, float f) {
+  constexpr int E = sizeof(G) + sizeof(O) == 4 ? 8 : 4;
+  constexpr int kTimes = kChunk / E / kThreads;
+  const uintptr_t off = (reinterpret_cast<uintptr_t>(p) % (E * sizeof(G))) |
+                        (reinterpret_cast<uintptr_t>(o) % (E * sizeof(O)));
+  if (off != 0 || n != kChunk) return scale_any(p, o, n, f);
+  const uint64_t f2 = lm::pack2(f, f);
+  Entries<G, E> x[kTimes];
+#pragma unroll
+  for (int u = 0; u < kTimes; ++u) x[u].load(p + (threadIdx.x + u * kThreads) * E);
+#pragma unroll
+  for (int u = 0; u < kTimes; ++u) {
+    Entries<O, E> r;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) r.put(i, lm::mul2(x[u].pair(i), f2));
+    r.store(o + (threadIdx.x + u * kThreads) * E);
+  }
+}
+
+// scale 0: the norms only
+template <int K>
+__global__ void __launch_bounds__(kThreads, 4) clip_scale(const __grid_constant__ Table<K> a, const double* slots,
+                                                          int64_t num_slots, float max_norm, float* stats,
+                                                          float* norms, uint32_t* flags, int scale) {
+  __shared__ double red[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  double sum = 0.0;
+  for (int64_t i = threadIdx.x; i < num_slots; i += kThreads) sum += slots[i];
+  const double norm = sqrt(block_sum_d(sum, red));
+  const bool finite = isfinite(norm);
+  const float f = finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    stats[0] = (float)norm;
+    stats[1] = f;
+    if (!finite && flags) atomicOr(flags, DOBB_FLAG_NONFINITE_G);
+  }
+  // every tensor's own norm: a warp each
+  const int lane = threadIdx.x & 31;
+  for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < a.num; t += gridDim.x * (kThreads / 32)) {
+    double s = 0.0;
+    if (a.chunk0[t + 1] > a.chunk0[t]) {
+      const int32_t last = cta_of(a, a.chunk0[t + 1] - 1);
+      for (int32_t b = cta_of(a, a.chunk0[t]) + lane; b <= last; b += 32) s += slots[a.slot0 + b + t];
+    }
+    s = warp_sum_d(s);
+    if (lane == 0) norms[t] = (float)sqrt(s);
+  }
+  if (!scale) return;
+  const int32_t b = blockIdx.x, first = first_chunk(a, b);
+  int32_t c = first_chunk(a, b + 1) - 1;
+  for (int t = c >= first ? tensor_of(a, c) : 0; c >= first; --t) {
+    const int32_t stop = max(first, a.chunk0[t]);
+    if (f == 1.f && a.out[t] == a.g[t]) c = min(c, stop - 1);  // in place and nothing to change
+    for (; c >= stop; --c) {
+      const int64_t lo = (int64_t)(c - a.chunk0[t]) * kChunk;
+      const int32_t n = (int32_t)min((int64_t)kChunk, a.numel[t] - lo);
+      const float* gf = static_cast<const float*>(a.g[t]) + lo;
+      const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(a.g[t]) + lo;
+      float* of = static_cast<float*>(a.out[t]) + lo;
+      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out[t]) + lo;
+      if (a.g_bf16[t]) {
+        if (a.out_bf16[t])
+          scale_chunk(gb, ob, n, f);
+        else
+          scale_chunk(gb, of, n, f);
+      } else if (a.out_bf16[t]) {
+        scale_chunk(gf, ob, n, f);
+      } else {
+        scale_chunk(gf, of, n, f);
+      }
+    }
+  }
+}
+
+int grid_of(int64_t chunks) { return (int)(chunks < 4 * kSms ? chunks : 4 * kSms); }
+
+// Slots of all launches; a launch takes up to kMaxTensors tensors.
+dobb_status measure(int num, const int64_t* numel, size_t* slots) {
   if (num < 1 || !numel)
     return fail(DOBB_ERR_INVALID_ARG, "num_tensors must be > 0 and numel non-NULL");
-  int64_t chunks = 0;
-  for (int i = 0; i < num; ++i) {
-    if (numel[i] < 0) return fail(DOBB_ERR_INVALID_ARG, "numel[%d] < 0", i);
-    chunks += chunks_of(numel[i]);
-    if (chunks > INT32_MAX) return fail(DOBB_ERR_UNSUPPORTED, "the tensors have too many entries");
+  size_t n = 0;
+  for (int t0 = 0; t0 < num; t0 += kMaxTensors) {
+    const int k = num - t0 < kMaxTensors ? num - t0 : kMaxTensors;
+    int64_t chunks = 0;
+    for (int i = t0; i < t0 + k; ++i) {
+      if (numel[i] < 0) return fail(DOBB_ERR_INVALID_ARG, "numel[%d] < 0", i);
+      chunks += chunks_of(numel[i]);
+      if (chunks > INT32_MAX) return fail(DOBB_ERR_UNSUPPORTED, "the tensors have too many entries");
+    }
+    n += grid_of(chunks) + k;
   }
-  w->chunks = chunks;
-  w->tensor_off = ((size_t)chunks * 8 + 255) / 256 * 256;
-  w->total = w->tensor_off + ((size_t)num * 8 + 255) / 256 * 256;
+  *slots = n;
   return DOBB_OK;
+}
+
+size_t slot_bytes(size_t slots) { return (slots * 8 + 255) / 256 * 256; }
+
+struct ClipCall {
+  int num;
+  const void* const* G;
+  const int32_t* grad_dtype;
+  const int64_t* numel;
+  float max_norm;
+  void* const* out;
+  const int32_t* out_dtype;
+  float* stats;
+  uint32_t* flags;
+  double* slots;
+  size_t num_slots;
+  cudaStream_t stream;
+};
+
+template <int K>
+cudaError_t run_clip(const ClipCall& r) {
+  Table<K> a;
+  for (int phase = 0; phase < 2; ++phase) {
+    a.slot0 = 0;
+    for (int t0 = 0; t0 < r.num; t0 += kMaxTensors) {
+      a.num = r.num - t0 < kMaxTensors ? r.num - t0 : kMaxTensors;
+      if (phase == 0 || r.num > kMaxTensors) {
+        a.chunk0[0] = 0;
+        for (int i = 0; i < a.num; ++i) {
+          a.g[i] = r.G[t0 + i];
+          a.out[i] = r.out ? r.out[t0 + i] : nullptr;
+          a.numel[i] = r.numel[t0 + i];
+          a.g_bf16[i] = r.grad_dtype[t0 + i] == DOBB_BF16;
+          a.out_bf16[i] = r.out && r.out_dtype[t0 + i] == DOBB_BF16;
+          a.chunk0[i + 1] = a.chunk0[i] + (int32_t)chunks_of(a.numel[i]);
+        }
+        a.chunks = a.chunk0[a.num];
+        a.grid = grid_of(a.chunks);
+      }
+      cudaLaunchConfig_t cfg{};
+      cfg.blockDim = dim3(kThreads);
+      cfg.stream = r.stream;
+      cudaError_t e = cudaSuccess;
+      if (phase == 0) {
+        cfg.gridDim = dim3((unsigned)a.grid);
+        if (a.grid > 0)
+          e = cudaLaunchKernelEx(&cfg, clip_sums<K>, a, r.slots);
+        else
+          e = cudaMemsetAsync(r.slots + a.slot0, 0, (size_t)a.num * 8, r.stream);
+      } else {
+        // beside the end of the sums, when it follows them at once
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = r.num <= kMaxTensors && a.grid > 0 ? 1 : 0;
+        const int norm_grid = (a.num + kThreads / 32 - 1) / (kThreads / 32);
+        cfg.gridDim = dim3((unsigned)(r.out && a.grid > 0 ? a.grid : norm_grid));
+        e = cudaLaunchKernelEx(&cfg, clip_scale<K>, a, (const double*)r.slots, (int64_t)r.num_slots, r.max_norm,
+                               r.stats, r.stats + 2 + t0, t0 == 0 ? r.flags : nullptr,
+                               (int)(r.out && a.grid > 0));
+      }
+      if (e != cudaSuccess) return e;
+      a.slot0 += a.grid + a.num;
+    }
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -132,16 +373,16 @@ dobb_status measure(int num, const int64_t* numel, Workspace* w) {
 using namespace dobb;
 
 extern "C" size_t dobb_clip_grads_bytes(int num, const int64_t* numel) {
-  Workspace w{};
-  return measure(num, numel, &w) == DOBB_OK ? w.total : 0;
+  size_t slots = 0;
+  return measure(num, numel, &slots) == DOBB_OK ? slot_bytes(slots) : 0;
 }
 
 extern "C" dobb_status dobb_clip_grads(int num, const void* const* G, const int32_t* grad_dtype,
                                        const int64_t* numel, float max_norm, void* const* out,
                                        const int32_t* out_dtype, float* stats, uint32_t* flags,
                                        void* ws, size_t ws_bytes, void* stream) {
-  Workspace w{};
-  dobb_status st = measure(num, numel, &w);
+  size_t slots = 0;
+  dobb_status st = measure(num, numel, &slots);
   if (st != DOBB_OK) return st;
   if (!G || !grad_dtype || (out && !out_dtype))
     return fail(DOBB_ERR_INVALID_ARG, "G, grad_dtype and (with out) out_dtype must be non-NULL");
@@ -160,43 +401,14 @@ extern "C" dobb_status dobb_clip_grads(int num, const void* const* G, const int3
   }
   if (!ws || lm::misaligned(ws, 256))
     return fail(DOBB_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
-  if (ws_bytes < w.total)
+  if (ws_bytes < slot_bytes(slots))
     return fail(DOBB_ERR_STATE, "workspace of %zu bytes is smaller than the %zu required", ws_bytes,
-                w.total);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  char* base = static_cast<char*>(ws);
-  double* tensor_sums = reinterpret_cast<double*>(base + w.tensor_off);
-  for (int phase = 0; phase < (out ? 2 : 1); ++phase) {
-    ClipArgs a;
-    a.chunk_base = 0;
-    a.chunk_sums = reinterpret_cast<double*>(base);
-    a.stats = stats;
-    for (int t0 = 0; t0 < num; t0 += kTensorsPerLaunch) {
-      a.num = num - t0 < kTensorsPerLaunch ? num - t0 : kTensorsPerLaunch;
-      a.tensor_sums = tensor_sums + t0;
-      a.chunk0[0] = 0;
-      for (int i = 0; i < a.num; ++i) {
-        a.g[i] = G[t0 + i];
-        a.out[i] = out ? out[t0 + i] : nullptr;
-        a.numel[i] = numel[t0 + i];
-        a.g_bf16[i] = grad_dtype[t0 + i] == DOBB_BF16;
-        a.out_bf16[i] = out && out_dtype[t0 + i] == DOBB_BF16;
-        a.chunk0[i + 1] = a.chunk0[i] + (int32_t)chunks_of(numel[t0 + i]);
-      }
-      const int32_t chunks = a.chunk0[a.num];
-      const int grid = chunks < 4096 ? chunks : 4096;
-      if (phase == 0) {
-        if (grid > 0) clip_chunk_sums<<<grid, kThreads, 0, s>>>(a);
-        clip_tensor_sums<<<a.num, kThreads, 0, s>>>(a);
-      } else if (grid > 0) {
-        clip_scale<<<grid, kThreads, 0, s>>>(a);
-      }
-      a.chunk_base += chunks;
-    }
-    if (phase == 0)
-      clip_finish<<<1, kThreads, 0, s>>>(tensor_sums, num, out ? max_norm : INFINITY, stats, flags);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "clipping launch: %s", cudaGetErrorString(e));
-  }
+                slot_bytes(slots));
+  const ClipCall r{num,   G,     grad_dtype, numel,
+                   out ? max_norm : INFINITY,
+                   out,   out_dtype, stats, flags, static_cast<double*>(ws),
+                   slots, static_cast<cudaStream_t>(stream)};
+  const cudaError_t e = num <= kFewTensors ? run_clip<kFewTensors>(r) : run_clip<kMaxTensors>(r);
+  if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "clipping launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
 }
