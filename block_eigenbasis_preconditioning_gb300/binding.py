@@ -90,10 +90,9 @@ SIGNATURES = [
     ("dobb_embedding_backward", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP,
                                            _c.c_int, _c.c_int64, _c.c_float, _VP, _c.c_int,
                                            _c.c_int64, _c.c_int, _VP, _VP, _c.c_size_t, _VP]),
-    ("dobb_clip_grads_bytes", _c.c_size_t, [_c.c_int, _I64P]),
-    ("dobb_clip_grads", _c.c_int, [_c.c_int, _c.POINTER(_VP), _c.POINTER(_c.c_int32), _I64P,
-                                   _c.c_float, _c.POINTER(_VP), _c.POINTER(_c.c_int32), _VP, _VP,
-                                   _VP, _c.c_size_t, _VP]),
+    ("dobb_clip_grads_bytes", _c.c_size_t, [_c.c_int, _VP]),
+    ("dobb_clip_grads", _c.c_int, [_c.c_int, _VP, _VP, _VP, _c.c_float, _VP, _VP, _VP, _VP, _VP,
+                                   _c.c_size_t, _VP]),
 ]
 
 

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
+from operator import attrgetter
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -31,16 +32,23 @@ MAX_TOP_K = 32
 
 class LogProbs(NamedTuple):
     """Result of `log_probs`, one entry per row (the alternatives: one row of
-    top_k).  row_max, log_sum and scale are what `log_probs_backward` needs:
-    lse = scale * row_max + log_sum."""
+    top_k).  stats, with the rows row_max and log_sum, and scale are what
+    `log_probs_backward` needs: lse = scale * row_max + log_sum."""
     logp: torch.Tensor
     lse: torch.Tensor
     entropy: Optional[torch.Tensor]
     top_ids: Optional[torch.Tensor]
     top_logp: Optional[torch.Tensor]
-    row_max: torch.Tensor
-    log_sum: torch.Tensor
+    stats: torch.Tensor
     scale: float
+
+    @property
+    def row_max(self) -> torch.Tensor:
+        return self.stats[0]
+
+    @property
+    def log_sum(self) -> torch.Tensor:
+        return self.stats[1]
 
 
 class GradNorm(NamedTuple):
@@ -168,7 +176,7 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
         with _On(index, stream, (logits, tokens, flags)):
             return log_probs(logits, tokens, scale=scale, top_k=top_k, entropy=entropy, flags=flags)
     dev = logits.device
-    # logp, lse, row_max, log_sum (, entropy): rows of one allocation
+    # rows of one allocation: row_max, log_sum, logp, lse (, entropy)
     f = torch.empty((5 if entropy else 4, rows), dtype=torch.float32, device=dev)
     p, ids, alt, ids_p, alt_p = f.data_ptr(), None, None, None, None
     if top_k:
@@ -177,10 +185,9 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
         ids_p, alt_p = ids.data_ptr(), alt.data_ptr()
     n = 4 * rows
     check(load_library().dobb_log_probs(
-        logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes, scale, top_k, p, p + n, p + 2 * n,
-        p + 3 * n, p + 4 * n if entropy else None, ids_p, alt_p, _flags(flags), _raw_stream(index)))
-    logp, lse, row_max, log_sum, *ent = f.unbind(0)
-    return LogProbs(logp, lse, ent[0] if entropy else None, ids, alt, row_max, log_sum, float(scale))
+        logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes, scale, top_k, p + 2 * n, p + 3 * n, p,
+        p + n, p + 4 * n if entropy else None, ids_p, alt_p, _flags(flags), _raw_stream(index)))
+    return LogProbs(f[2], f[3], f[4] if entropy else None, ids, alt, f[:2], float(scale))
 
 
 def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogProbs, grad_logp: torch.Tensor, *,
@@ -197,12 +204,13 @@ def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogPr
         raise ValueError(f"{tokens.numel()} tokens for {rows} rows")
     if grad_entropy is not None and result.entropy is None:
         raise ValueError("grad_entropy needs a result with the entropy")
-    index = _device(logits, tokens, grad_logp, grad_entropy, grad_lse, out, result.row_max)
+    index = _device(logits, tokens, grad_logp, grad_entropy, grad_lse, out, result.stats)
     if _elsewhere(index, stream):
-        with _On(index, stream, (logits, tokens, out, grad_logp, grad_entropy, grad_lse, result.row_max, result.log_sum,
+        with _On(index, stream, (logits, tokens, out, grad_logp, grad_entropy, grad_lse, result.stats,
                                  result.entropy)):
             return log_probs_backward(logits, tokens, result, grad_logp, grad_entropy=grad_entropy, grad_lse=grad_lse, out=out)
-    args = [_vector(result.row_max, rows, "row_max"), _vector(result.log_sum, rows, "log_sum"),
+    stats = _vector(result.stats, 2 * rows, "stats")
+    args = [stats, stats + 4 * rows,
             _vector(result.entropy if grad_entropy is not None else None, rows, "entropy"),
             _vector(grad_logp, rows, "grad_logp"), _vector(grad_entropy, rows, "grad_entropy"),
             _vector(grad_lse, rows, "grad_lse")]
@@ -314,16 +322,22 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _dtype_codes(tensors, what: str):
-    try:
-        return array("i", [_DTYPES[t.dtype] for t in tensors])
-    except KeyError as e:
-        raise ValueError(f"every {what} must be float32 or bfloat16, got {e.args[0]}") from None
+_dtype_of = attrgetter("dtype")
 
 
-def _at(a: array, kind):
-    """A ctypes pointer to an array's values."""
-    return ctypes.cast(a.buffer_info()[0], ctypes.POINTER(kind))
+def _dtype_codes(tensors, what: str) -> array:
+    kinds = set(map(_dtype_of, tensors))
+    for d in kinds:
+        if d not in _DTYPES:
+            raise ValueError(f"every {what} must be float32 or bfloat16, got {d}")
+    if len(kinds) == 1:
+        return array("i", (_DTYPES[kinds.pop()],)) * len(tensors)
+    return array("i", [_DTYPES[t.dtype] for t in tensors])
+
+
+def _same_device(tensors, index: int) -> None:
+    if set(map(torch.Tensor.get_device, tensors)) != {index}:
+        raise ValueError(f"all tensors must be on cuda:{index}")
 
 
 def _clip(grads: Sequence[torch.Tensor], max_norm: float, outs: Optional[Sequence[torch.Tensor]],
@@ -332,41 +346,41 @@ def _clip(grads: Sequence[torch.Tensor], max_norm: float, outs: Optional[Sequenc
     if n == 0:
         raise ValueError("no gradients given")
     in_place = outs is grads
-    index = _device(*grads, flags)
+    index = _device(grads[0], flags)
+    _same_device(grads, index)
     gd = _dtype_codes(grads, "gradient")
     plain = all(map(torch.Tensor.is_contiguous, grads))
     if not plain and not all(map(_dense, grads)):
         raise ValueError("every gradient must be dense")
+    ne = array("q", map(torch.Tensor.numel, grads))
     od = gd
     if outs is not None and not in_place:
-        if len(outs) != n:
-            raise ValueError(f"{len(outs)} outputs for {n} gradients")
-        _device(grads[0], *outs)
+        if len(outs) != n or array("q", map(torch.Tensor.numel, outs)) != ne:
+            raise ValueError("there must be an output of the same size for every gradient")
+        _same_device(outs, index)
         od = _dtype_codes(outs, "output")
-        if not all(g.shape == o.shape for g, o in zip(grads, outs)):
-            raise ValueError("every output must have its gradient's shape")
         if not (plain and all(map(torch.Tensor.is_contiguous, outs))) and not all(
-                g.stride() == o.stride() or (g.is_contiguous() and o.is_contiguous()) for g, o in zip(grads, outs)):
-            raise ValueError("every output must have its gradient's strides")
+                (g.shape == o.shape and g.stride() == o.stride()) or (g.is_contiguous() and o.is_contiguous())
+                for g, o in zip(grads, outs)):
+            raise ValueError("every output must be laid out like its gradient")
     if _elsewhere(index, stream):
         with _On(index, stream, [*grads, *(outs or ()), flags]):
             return _clip(grads, max_norm, outs, flags, None)
     lib = load_library()
     gp = array("Q", map(torch.Tensor.data_ptr, grads))
-    ne = array("q", map(torch.Tensor.numel, grads))
     op = None if outs is None else gp if in_place else array("Q", map(torch.Tensor.data_ptr, outs))
-    sizes = _at(ne, ctypes.c_int64)
+    sizes = ne.buffer_info()[0]
     nbytes = lib.dobb_clip_grads_bytes(n, sizes)
     if nbytes == 0:
         check(1)
-    dev = grads[0].device
-    stats = torch.empty((2 + n,), dtype=torch.float32, device=dev)
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    # the statistics, and behind them the workspace, in one allocation
+    at = (8 + 4 * n + 255) // 256 * 64
+    stats = torch.empty((at + (nbytes + 3) // 4,), dtype=torch.float32, device=grads[0].device)
+    p = stats.data_ptr()
     check(lib.dobb_clip_grads(
-        n, _at(gp, ctypes.c_void_p), _at(gd, ctypes.c_int32), sizes, max_norm, None if op is None else _at(op, ctypes.c_void_p),
-        None if op is None else _at(od, ctypes.c_int32), stats.data_ptr(), _flags(flags), ws.data_ptr(), nbytes,
-        _raw_stream(index)))
-    return GradNorm(stats[0], stats[1], stats[2:])
+        n, gp.buffer_info()[0], gd.buffer_info()[0], sizes, max_norm, None if op is None else op.buffer_info()[0],
+        None if op is None else od.buffer_info()[0], p, _flags(flags), p + 4 * at, nbytes, _raw_stream(index)))
+    return GradNorm(stats[0], stats[1], stats[2:2 + n])
 
 
 def grad_norm(grads: Sequence[torch.Tensor], *, flags: Optional[torch.Tensor] = None,
@@ -378,8 +392,8 @@ def grad_norm(grads: Sequence[torch.Tensor], *, flags: Optional[torch.Tensor] = 
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
                flags: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> GradNorm:
     """Scale the gradients by min(1, max_norm / norm), norm the l2 norm over
-    all of them: in place, or into `out` (same shapes, float32 or bfloat16
-    each: for instance fp32 accumulators into the bf16 gradients that
+    all of them: in place, or into `out` (as many entries each, laid out alike,
+    float32 or bfloat16: for instance fp32 accumulators into the bf16 gradients that
     `Dobb.step` takes).  When the norm is not finite the gradients are passed
     on unscaled and flag 2 (non-finite gradient) is set in `flags`.
 
