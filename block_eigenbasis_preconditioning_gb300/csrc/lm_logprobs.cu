@@ -10,6 +10,7 @@
 #include <cooperative_groups.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "lm_common.cuh"
 #include "tc_ptx.cuh"
@@ -67,8 +68,9 @@ struct LpGradArgs {
 
 constexpr int kFwdThreads = 256;
 constexpr int kFwdWarps = kFwdThreads / 32;
+constexpr int kSmallThreads = 64;
+
 constexpr int kUnroll = 4;
-constexpr int kSegs = kFwdThreads;
 constexpr int kPieces = 8;  // parts of a thread's entries that have a maximum of their own
 constexpr int kList = 128;
 constexpr int kHits = 64;
@@ -93,10 +95,11 @@ struct TopScratch {
   uint4 hit[kHits];
 };
 
+template <int NT>
 struct FwdShared {
   Sums part;  // of this CTA's slice of the row
-  float warp_m[kFwdWarps], warp_s[kFwdWarps], warp_e[kFwdWarps];
-  uint32_t seg[kSegs];  // key of every thread's maximum
+  float warp_m[NT / 32], warp_s[NT / 32], warp_e[NT / 32];
+  uint32_t seg[NT];  // key of every thread's maximum
   TopScratch top;
 };
 
@@ -146,13 +149,13 @@ __device__ __forceinline__ void order_desc(uint32_t& a, uint32_t& b) {
 
 // The largest top_k keys of the slice x[0 .. n), which starts at index j0 of
 // the row, into sh.best; seg: the key of every segment's maximum, visible to
-// all.  Segment s holds the vectors s, s + kSegs, ...; the first warp's lanes
+// all.  Segment s of kSegs holds the vectors s, s + kSegs, ...; the first warp's lanes
 // hold the entries outside the vectors (sval at sat, sat < 0 for none).
 // pieces, if given: for every piece_vecs vectors of a segment (piece p of
 // segment s at p * kSegs + s) the upper half of a number that none of them
 // exceeds; then only the pieces that may hold something are read again.  Runs
 // on NW warps (the whole block, or one warp of it).
-template <typename T, int NW>
+template <typename T, int kSegs, int NW>
 __device__ __forceinline__ void slice_top(TopScratch& sh, const uint32_t* seg, const T* x, int32_t n,
                                           int32_t j0, int32_t head, int32_t nvec, int32_t sat,
                                           float sval, const uint16_t* pieces, int32_t piece_vecs,
@@ -168,7 +171,7 @@ __device__ __forceinline__ void slice_top(TopScratch& sh, const uint32_t* seg, c
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
   if (warp == 0) {
     constexpr int P = kSegs / 32;
-    static_assert(P == 8, "the sorting network below sorts 8 values");
+    static_assert(P == 2 || P == 8, "the sorting network below sorts 2 or 8 values");
     uint32_t s[P], keep[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) keep[i] = s[i] = seg[i * 32 + lane];
@@ -176,18 +179,20 @@ __device__ __forceinline__ void slice_top(TopScratch& sh, const uint32_t* seg, c
     // the largest of the lanes' first values is taken away top_k times
 #pragma unroll
     for (int i = 0; i < P; i += 2) order_desc(s[i], s[i + 1]);
+    if constexpr (P == 8) {
 #pragma unroll
-    for (int i = 0; i < P; i += 4) {
-      order_desc(s[i], s[i + 2]);
-      order_desc(s[i + 1], s[i + 3]);
-      order_desc(s[i + 1], s[i + 2]);
+      for (int i = 0; i < P; i += 4) {
+        order_desc(s[i], s[i + 2]);
+        order_desc(s[i + 1], s[i + 3]);
+        order_desc(s[i + 1], s[i + 2]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) order_desc(s[i], s[i + 4]);
+      order_desc(s[2], s[4]);
+      order_desc(s[3], s[5]);
+#pragma unroll
+      for (int i = 1; i < P - 1; i += 2) order_desc(s[i], s[i + 1]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) order_desc(s[i], s[i + 4]);
-    order_desc(s[2], s[4]);
-    order_desc(s[3], s[5]);
-#pragma unroll
-    for (int i = 1; i < P - 1; i += 2) order_desc(s[i], s[i + 1]);
     uint32_t bound = kNegInfKey;
     for (int r = 0; r < top_k; ++r) {
       bound = __reduce_max_sync(0xffffffffu, s[0]);
@@ -420,8 +425,8 @@ __device__ __forceinline__ float add_vectors(const uint4 (&v)[U], float c, uint6
 }
 
 // Maximum, sums and the largest keys of one slice, into sh.part and sh.best
-template <typename T, bool ENT>
-__device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, float c, int top_k) {
+template <typename T, bool ENT, int NT>
+__device__ __forceinline__ void slice_forward(FwdShared<NT>& sh, const T* x, int32_t n, int32_t j0, float c, int top_k) {
   using V = lm::Vec16<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t head = (int32_t)lm::head_of(x, n), nvec = (n - head) / V::N;
@@ -431,13 +436,13 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
   uint64_t s2 = 0, e2 = 0;
   const uint64_t c2 = lm::pack2(c, c);
   int32_t j = tid;
-  for (; j + (kUnroll - 1) * kFwdThreads < nvec; j += kUnroll * kFwdThreads) {
+  for (; j + (kUnroll - 1) * NT < nvec; j += kUnroll * NT) {
     uint4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(xv + j + u * kFwdThreads);
+    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(xv + j + u * NT);
     add_vectors<T, ENT>(v, c, c2, own, r, s2, e2, nan);
   }
-  for (; j < nvec; j += kFwdThreads) {
+  for (; j < nvec; j += NT) {
     const uint4 v[1] = {__ldg(xv + j)};
     add_vectors<T, ENT>(v, c, c2, own, r, s2, e2, nan);
   }
@@ -473,11 +478,11 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
   __syncthreads();
   m = sh.warp_m[0];
 #pragma unroll
-  for (int w = 1; w < kFwdWarps; ++w) m = fmaxf(m, sh.warp_m[w]);
+  for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, sh.warp_m[w]);
   const float to = reference(m, c);
   if (fabsf(m) != INFINITY && fabsf(m * c) == INFINITY) {
     s = e = 0.f;
-    for (int32_t i = tid; i < n; i += kFwdThreads) {
+    for (int32_t i = tid; i < n; i += NT) {
       const float w = lm::max_nan((load_f32(x + i) - m) * c, -200.f), p = lm::exp2_fast(w);
       s += p;
       e += p * w;
@@ -499,7 +504,7 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
   if (tid == 0) {
     Sums t{m, to, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kFwdWarps; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       t.s += sh.warp_s[w];
       t.e += sh.warp_e[w];
     }
@@ -508,7 +513,7 @@ __device__ void slice_forward(FwdShared& sh, const T* x, int32_t n, int32_t j0, 
   if (top_k > 0) {
     sh.seg[tid] = order_key(nan ? NAN : own);
     __syncthreads();
-    slice_top<T, kFwdWarps>(sh.top, sh.seg, x, n, j0, head, nvec, sat, sval, nullptr, 0, top_k);
+    slice_top<T, NT, NT / 32>(sh.top, sh.seg, x, n, j0, head, nvec, sat, sval, nullptr, 0, top_k);
   }
 }
 
@@ -538,9 +543,9 @@ __device__ __forceinline__ float write_row(const LpArgs& a, int64_t row, const S
 
 // One cluster of CTAs per row (one CTA when the rows fill the GPU): every CTA
 // takes a slice of the row, the first one joins the slices.
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
-  __shared__ FwdShared sh;
+template <typename T, bool ENT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
+  __shared__ FwdShared<NT> sh;
   __shared__ unsigned long long all[kMaxCluster * DOBB_MAX_TOP_K];
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
     tok = lm::load_token(a.tokens, a.token_bytes, row);
     if (tok >= 0 && tok < a.vocab) given = load_f32(x + tok);
   }
-  slice_forward<T, ENT>(sh, x + lo, n, lo, a.scale * kLog2e, a.top_k);
+  slice_forward<T, ENT, NT>(sh, x + lo, n, lo, a.scale * kLog2e, a.top_k);
   if (parts > 1) cluster.sync();
   if (rank == 0) {
     if (threadIdx.x == 0) {
@@ -585,10 +590,10 @@ __global__ void __launch_bounds__(kFwdThreads, 4) lp_forward(const LpArgs a) {
     if (a.top_k > 0) {
       // the slices' keys: a key's rank among them is its place
       const int num = parts * a.top_k;
-      for (int i = threadIdx.x; i < num; i += kFwdThreads)
+      for (int i = threadIdx.x; i < num; i += NT)
         all[i] = parts > 1 ? cluster.map_shared_rank(&sh, i / a.top_k)->top.best[i % a.top_k] : sh.top.best[i];
       __syncthreads();
-      for (int i = threadIdx.x; i < num; i += kFwdThreads) {
+      for (int i = threadIdx.x; i < num; i += NT) {
         const unsigned long long mine = all[i];
         int at = i;
         if (parts > 1) {
@@ -624,8 +629,8 @@ struct RingShared {
   uint64_t full[kStages], empty[kStages], row_full[kJoinWarps], row_empty[kJoinWarps];
   int32_t abort;
   Sums stat[kJoinWarps][kFwdWarps];
-  uint32_t seg[kJoinWarps][kSegs];  // key of every thread's maximum
-  uint16_t pieces[kJoinWarps][kPieces * kSegs];
+  uint32_t seg[kJoinWarps][kFwdThreads];  // key of every thread's maximum
+  uint16_t pieces[kJoinWarps][kPieces * kFwdThreads];
   TopScratch top[kJoinWarps];
 };
 
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
         }
         if (a.top_k > 0 && (--left == 0 || v0 + kStageVecs >= nvec)) {
           *pieces = upper_half(piece);
-          pieces += kSegs;
+          pieces += kFwdThreads;
           piece = -INFINITY;
           left = fold;
         }
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
       if (a.top_k > 0) {
         log_sum = __shfl_sync(0xffffffffu, log_sum, 0);
         const bool empty = m == -INFINITY && t.s == 0.f;
-        slice_top<T, 1>(top, sh.seg[buf], x, a.vocab, 0, head, nvec, at, single, sh.pieces[buf],
+        slice_top<T, kFwdThreads, 1>(top, sh.seg[buf], x, a.vocab, 0, head, nvec, at, single, sh.pieces[buf],
                         (nvec / kStageVecs / kPieces + 1) * kUnroll, a.top_k);
         if (lane < a.top_k) {
           const unsigned long long key = top.best[lane];
@@ -937,7 +942,17 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
   if (top_k > 0 && (!top_ids || !top_logp))
     return fail(DOBB_ERR_INVALID_ARG, "top_ids and top_logp must be non-NULL when top_k > 0");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (rows >= 2 * kSms && vocab * (int64_t)lm::dtype_bytes(logits_dtype) >= 32768 && vocab <= (1 << 20)) {
+  // Which form, measured (us; bf16 rows with 5 alternatives unless said):
+  //   4000 rows of 24 KB   ring 32, blocks of 64 threads 38, of 256 threads 47
+  //   4000 rows of 12 KB (fp32)  ring 22, 64 threads 24, 256 threads 35
+  //   400 rows of 24 KB    ring 7.8, 256 threads 7.5 (20 alternatives: 11.2, 9.0)
+  //   150 rows of 100 KB   one block a row 9.9, two 16.6
+  //   64 fp32 rows of 513 KB  clusters of 4 11.3, of 8 11.0
+  const int64_t row_bytes = vocab * (int64_t)lm::dtype_bytes(logits_dtype);
+  // (the ring's waits are bounded; one warp searches a whole row when nearly
+  // all of it ties, which stays below the limit for rows of 2^20 entries)
+  if (vocab <= (1 << 20) &&
+      ((rows >= 2 * kSms && row_bytes >= 32768) || (rows >= 4 * kSms && row_bytes >= 8192))) {
     const LpArgs a{logits, row_stride, (int32_t)vocab, tokens,  token_bytes, scale,    top_k, logp,
                    lse,    row_max,    log_sum,        entropy, top_ids,     top_logp, flags};
     const size_t smem = (size_t)kStages * kStageVecs * 16 + sizeof(RingShared);
@@ -957,6 +972,7 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
   }
   int parts = 1;
   while (parts < kMaxCluster && rows * parts < kSms && vocab / parts > 4096) parts *= 2;
+  const bool small = rows >= 4 * kSms && row_bytes < 8192;
   // a launch holds up to 2^31 - 1 blocks
   const int64_t most = ((int64_t)1 << 30) / parts;
   cudaError_t e = cudaSuccess;
@@ -969,19 +985,22 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
              top_ids ? top_ids + r0 * top_k : nullptr, top_logp ? top_logp + r0 * top_k : nullptr, flags};
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(nr * parts));
-    cfg.blockDim = dim3(kFwdThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {(unsigned)parts, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (logits_dtype == DOBB_F32)
-      e = entropy ? cudaLaunchKernelEx(&cfg, lp_forward<float, true>, a)
-                  : cudaLaunchKernelEx(&cfg, lp_forward<float, false>, a);
-    else
-      e = entropy ? cudaLaunchKernelEx(&cfg, lp_forward<__nv_bfloat16, true>, a)
-                  : cudaLaunchKernelEx(&cfg, lp_forward<__nv_bfloat16, false>, a);
+    auto launch = [&](auto threads) {
+      constexpr int NT = decltype(threads)::value;
+      cfg.blockDim = dim3(NT);
+      if (logits_dtype == DOBB_F32)
+        return entropy ? cudaLaunchKernelEx(&cfg, lp_forward<float, true, NT>, a)
+                       : cudaLaunchKernelEx(&cfg, lp_forward<float, false, NT>, a);
+      return entropy ? cudaLaunchKernelEx(&cfg, lp_forward<__nv_bfloat16, true, NT>, a)
+                     : cudaLaunchKernelEx(&cfg, lp_forward<__nv_bfloat16, false, NT>, a);
+    };
+    e = small ? launch(std::integral_constant<int, kSmallThreads>{}) : launch(std::integral_constant<int, kFwdThreads>{});
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "log-probability launch: %s", cudaGetErrorString(e));

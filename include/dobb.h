@@ -363,7 +363,7 @@ const char* dobb_eigh_noalloc_last_error(void);
 
 /* Log probabilities of given tokens, entropies and the most likely
  * alternatives.  With y_j = scale * logits[r][j], j < vocab:
- *   row_max[r] = max_j logits[r][j]
+ *   row_max[r] = max_j logits[r][j] (NaN are passed over)
  *   log_sum[r] = log sum_j exp(scale * (logits[r][j] - row_max[r]))
  *   lse[r]     = scale * row_max[r] + log_sum[r]
  *   logp[r]    = y_t - lse[r],  t = tokens[r]

@@ -34,7 +34,7 @@ def log_probs(logits: np.ndarray, tokens: np.ndarray, scale: float = 1.0, top_k:
     for i in range(rows):
         x = logits[i].astype(np.float64)
         bad = bool(np.any(np.isnan(x)) or np.any(x == np.inf))
-        m = np.nan if np.all(np.isnan(x)) else float(np.nanmax(x))
+        m = float(np.max(x[~np.isnan(x)], initial=-np.inf))  # NaN are passed over
         if bad:
             log_sum = lse = ent = math.nan
             lp = np.full(len(x), math.nan)

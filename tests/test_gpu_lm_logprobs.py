@@ -90,6 +90,22 @@ def test_alternatives_with_many_ties(dtype, k, vocab):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab,k", [(1, 1), (5, 5), (33, 32), (700, 9), (2050, 32), (4093, 3)])
+def test_many_short_rows(dtype, vocab, k):
+    rng = np.random.default_rng(vocab)
+    rows = 640
+    x = rounded(rng.standard_normal((rows, vocab)) * 2, dtype)
+    x[1::5] = rng.integers(-1, 2, x[1::5].shape)          # ties
+    x[2::10] = -np.inf
+    x[3::10, 1:] = float(torch.finfo(TORCH[dtype]).min)
+    x[4::10, vocab // 2] = np.nan
+    x[5::10, : vocab // 2] = -np.inf
+    t = rng.integers(-1, vocab, rows)
+    _, _, r = _forward(x, t, dtype, 0.9, k, 1, 1)
+    _check_forward(x, t, r, float(np.float32(0.9)), k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("k", [1, 9, 32])
 def test_alternatives_with_many_ties_over_many_long_rows(dtype, k):
     rng = np.random.default_rng(k)
