@@ -9,7 +9,6 @@
 // (E + S d) e^d.  An entry -inf adds nothing to either sum.
 #include <cooperative_groups.h>
 
-#include <cfloat>
 #include <type_traits>
 
 #include "lm_common.cuh"
@@ -56,20 +55,21 @@ struct LpGradArgs {
 // multiply-add: the reference R is M c rounded, and taken as exact from there
 // on, so the rounding costs nothing.  An entry far below M is clamped to
 // v = -200, where 2^v is 0, so that -inf adds 0 * -200 and not 0 * -inf.
-// Where M c leaves the range of fp32 (masks of the type's lowest value and
-// nothing else in the row) the slice is summed again as 2^{(x - M) c}.
+// R is kept above -2^31, and rounds by at most 64 below 2^31, so no sum
+// overflows for it.  Where the maximum of a whole slice lies beyond (a row of
+// masks like -1e30 or the type's lowest value, and nothing else) the slice is
+// summed again as 2^{(x - M) c}.  In the end the sums refer to M c itself.
 //
 // The alternatives cost no second pass: the k-th largest of the segments'
 // maxima (a segment: the entries of one thread) is a lower bound
 // of the k-th largest entry, so only segments whose maximum reaches it are
 // read again (about k of them, from L2), and their entries that reach it are
-// ranked by counting.  When more entries than the list holds reach the bound
-// (many equal logits), the largest remaining key is searched k times instead.
+// ranked by counting.  Among many equal logits, those above the bound are taken
+// and then the first ones equal to it.
 
 constexpr int kFwdThreads = 256;
 constexpr int kFwdWarps = kFwdThreads / 32;
 constexpr int kSmallThreads = 64;
-
 constexpr int kUnroll = 4;
 constexpr int kPieces = 8;  // parts of a thread's entries that have a maximum of their own
 constexpr int kList = 128;
@@ -80,8 +80,8 @@ constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Sums {
-  float m, r;  // the maximum, and what s and e refer to
-  float s, e;  // e in units of log 2
+  float m;     // the maximum
+  float s, e;  // relative to it, e in units of log 2
 };
 
 struct TopScratch {
@@ -130,15 +130,25 @@ __device__ __forceinline__ int32_t key_index(unsigned long long k) {
   return 0x7fffffff - (int32_t)(uint32_t)k;
 }
 
-// R of a maximum; a slice of -inf alone, or of values whose product with c
-// overflows, gets the lowest number
-__device__ __forceinline__ float reference(float m, float c) { return fmaxf(m * c, -FLT_MAX); }
+// R of a maximum, kept in a range where a sum relative to it cannot overflow;
+// wide: the maximum of a slice lies outside it
+constexpr float kWide = 2147483648.f;
+__device__ __forceinline__ float reference(float m, float c) { return fmaxf(m * c, -kWide); }
+__device__ __forceinline__ bool is_wide(float m, float c) {
+  return fabsf(m) != INFINITY && !(fabsf(m * c) < kWide);
+}
 
-// the sums relative to a larger reference
-__device__ __forceinline__ void raise_to(float& s, float& e, float from, float to) {
-  const float d = lm::max_nan(from - to, -1000.f), f = lm::exp2_fast(d);
+// the sums relative to a reference that is d larger (-d)
+__device__ __forceinline__ void move_by(float& s, float& e, float d) {
+  d = lm::max_nan(d, -1000.f);
+  const float f = lm::exp2_fast(d);
   e = (e + s * d) * f;
   s *= f;
+}
+
+// from relative to R = reference(m, c) to relative to m c
+__device__ __forceinline__ void move_to_max(float& s, float& e, float r, float m, float c) {
+  if (fabsf(m) != INFINITY) move_by(s, e, -fmaf(m, c, -r));
 }
 
 __device__ __forceinline__ void order_desc(uint32_t& a, uint32_t& b) {
@@ -149,8 +159,9 @@ __device__ __forceinline__ void order_desc(uint32_t& a, uint32_t& b) {
 
 // The largest top_k keys of the slice x[0 .. n), which starts at index j0 of
 // the row, into sh.best; seg: the key of every segment's maximum, visible to
-// all.  Segment s of kSegs holds the vectors s, s + kSegs, ...; the first warp's lanes
-// hold the entries outside the vectors (sval at sat, sat < 0 for none).
+// all.  Segment s of kSegs holds the vectors s, s + kSegs, ...; the first
+// warp's lanes hold the entries outside the vectors (sval at sat, sat < 0 for
+// none).
 // pieces, if given: for every piece_vecs vectors of a segment (piece p of
 // segment s at p * kSegs + s) the upper half of a number that none of them
 // exceeds; then only the pieces that may hold something are read again.  Runs
@@ -431,7 +442,7 @@ __device__ __forceinline__ void slice_forward(FwdShared<NT>& sh, const T* x, int
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t head = (int32_t)lm::head_of(x, n), nvec = (n - head) / V::N;
   const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  float own = -INFINITY, r = -FLT_MAX, s, e;
+  float own = -INFINITY, r = -kWide, s, e;
   bool nan = false;
   uint64_t s2 = 0, e2 = 0;
   const uint64_t c2 = lm::pack2(c, c);
@@ -462,7 +473,7 @@ __device__ __forceinline__ void slice_forward(FwdShared<NT>& sh, const T* x, int
     nan |= !(sval == sval);
     if (sval > own) {
       const float to = reference(sval, c);
-      raise_to(s, e, r, to);
+      move_by(s, e, r - to);
       own = sval;
       r = to;
     }
@@ -479,16 +490,18 @@ __device__ __forceinline__ void slice_forward(FwdShared<NT>& sh, const T* x, int
   m = sh.warp_m[0];
 #pragma unroll
   for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, sh.warp_m[w]);
-  const float to = reference(m, c);
-  if (fabsf(m) != INFINITY && fabsf(m * c) == INFINITY) {
+  if (is_wide(m, c)) {
     s = e = 0.f;
+#pragma unroll 4
     for (int32_t i = tid; i < n; i += NT) {
       const float w = lm::max_nan((load_f32(x + i) - m) * c, -200.f), p = lm::exp2_fast(w);
       s += p;
       e += p * w;
     }
   } else {
-    raise_to(s, e, r, to);
+    const float to = reference(m, c);
+    move_by(s, e, r - to);
+    move_to_max(s, e, to, m, c);
   }
   if (nan) s = NAN;
 #pragma unroll
@@ -502,7 +515,7 @@ __device__ __forceinline__ void slice_forward(FwdShared<NT>& sh, const T* x, int
   }
   __syncthreads();
   if (tid == 0) {
-    Sums t{m, to, 0.f, 0.f};
+    Sums t{m, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
       t.s += sh.warp_s[w];
@@ -521,11 +534,8 @@ __device__ __forceinline__ void slice_forward(FwdShared<NT>& sh, const T* x, int
 template <bool ENT>
 __device__ __forceinline__ float write_row(const LpArgs& a, int64_t row, const Sums& r, int64_t tok,
                                            float given) {
-  const float c = a.scale * kLog2e;
   const bool empty = r.m == -INFINITY && r.s == 0.f;
-  // the sums refer to r.r, the result to the maximum
-  const float off = fabsf(r.m * c) == INFINITY ? 0.f : -fmaf(r.m, c, -r.r);
-  const float log_sum = kLn2 * (log2f(r.s) + off);
+  const float log2_sum = log2f(r.s), log_sum = kLn2 * log2_sum;
   float lp = 0.f;
   if (tok >= a.vocab) {
     lp = NAN;
@@ -537,7 +547,7 @@ __device__ __forceinline__ float write_row(const LpArgs& a, int64_t row, const S
   a.row_max[row] = r.m;
   a.log_sum[row] = log_sum;
   if (a.lse) a.lse[row] = empty ? -INFINITY : a.scale * r.m + log_sum;
-  if (ENT) a.entropy[row] = empty ? 0.f : kLn2 * (log2f(r.s) - r.e / r.s);
+  if (ENT) a.entropy[row] = empty ? 0.f : kLn2 * (log2_sum - r.e / r.s);
   return log_sum;
 }
 
@@ -569,23 +579,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
       const float c = a.scale * kLog2e;
       if (parts > 1) {
         for (int p = 1; p < parts; ++p) r.m = fmaxf(r.m, cluster.map_shared_rank(&sh, p)->part.m);
-        const float m = r.m, to = reference(m, c);
-        r = Sums{m, to, 0.f, 0.f};
-        const bool wide = fabsf(m) != INFINITY && fabsf(m * c) == INFINITY;
+        const float m = r.m;
+        r = Sums{m, 0.f, 0.f};
         for (int p = 0; p < parts; ++p) {
           Sums q = cluster.map_shared_rank(&sh, p)->part;
-          if (wide) {
-            raise_to(q.s, q.e, (q.m - m) * c, 0.f);
-          } else {
-            raise_to(q.s, q.e, q.r, to);
-          }
+          if (q.m != m) move_by(q.s, q.e, (q.m - m) * c);
           r.s += q.s;
           r.e += q.e;
         }
       }
       const float log_sum = write_row<ENT>(a, row, r, tok, given);
       const bool empty = r.m == -INFINITY && r.s == 0.f;
-      sh.part = Sums{r.m, log_sum, empty ? 1.f : 0.f, 0.f};
+      sh.part = Sums{r.m, log_sum, empty ? 1.f : 0.f};
     }
     if (a.top_k > 0) {
       // the slices' keys: a key's rank among them is its place
@@ -601,10 +606,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
           for (int o = 0; o < num; ++o) at += all[o] > mine;
         }
         if (mine != 0 && at < a.top_k) {
-          const bool empty = sh.part.s != 0.f;
+          const bool empty = sh.part.e != 0.f;
           a.top_ids[row * a.top_k + at] = key_index(mine);
           a.top_logp[row * a.top_k + at] =
-              empty ? -INFINITY : a.scale * (key_value((uint32_t)(mine >> 32)) - sh.part.m) - sh.part.r;
+              empty ? -INFINITY : a.scale * (key_value((uint32_t)(mine >> 32)) - sh.part.m) - sh.part.s;
         }
       }
     }
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
 // Persistent blocks take the rows in turn.  One thread streams them through a
 // ring of shared memory with bulk copies, so that the next rows are on their
 // way whatever the other warps do; eight warps keep the maxima and sums, each
-// at its own pace; two more warps, row about, join them, find the alternatives
+// at its own pace; three more warps, row about, join them, find the alternatives
 // and write the row while the eight are in the next ones.
 constexpr int kStageVecs = kUnroll * kFwdThreads;
 constexpr int kStages = 3;
@@ -628,13 +633,13 @@ constexpr int kRingBlocks = 3;  // per SM
 struct RingShared {
   uint64_t full[kStages], empty[kStages], row_full[kJoinWarps], row_empty[kJoinWarps];
   int32_t abort;
-  Sums stat[kJoinWarps][kFwdWarps];
+  float4 stat[kJoinWarps][kFwdWarps];  // maximum, reference, and the sums relative to that
   uint32_t seg[kJoinWarps][kFwdThreads];  // key of every thread's maximum
   uint16_t pieces[kJoinWarps][kPieces * kFwdThreads];
   TopScratch top[kJoinWarps];
 };
 
-// Wait for a phase; false once a wait of this block has run out of time.
+// Wait for a phase; false once a wait of this block has run out of time (2 s).
 __device__ __forceinline__ bool ring_wait(RingShared& sh, uint64_t* bar, uint32_t parity) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::global_timer_ns();
@@ -646,6 +651,11 @@ __device__ __forceinline__ bool ring_wait(RingShared& sh, uint64_t* bar, uint32_
     }
   }
   return true;
+}
+
+// the same for a whole warp: all of it goes on, or none
+__device__ __forceinline__ bool ring_wait_warp(RingShared& sh, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, ring_wait(sh, bar, parity));
 }
 
 template <typename T, bool ENT>
@@ -678,17 +688,17 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, ++i) {
       const T* x = logits + row * a.row_stride;
       const int32_t head = (int32_t)lm::head_of(x, a.vocab), nvec = (a.vocab - head) / V::N;
-      float own = -INFINITY, r = -FLT_MAX, piece = -INFINITY;
+      float own = -INFINITY, r = -kWide, piece = -INFINITY;
       bool nan = false;
       uint64_t s2 = 0, e2 = 0;
       const uint32_t buf = i % kJoinWarps;
       const int fold = nvec / kStageVecs / kPieces + 1;  // stages per piece
       int left = fold;
       uint16_t* pieces = sh.pieces[buf] + mtid;
-      if (i >= kJoinWarps && !ring_wait(sh, &sh.row_empty[buf], ((i / kJoinWarps) & 1) ^ 1)) return;
+      if (i >= kJoinWarps && !ring_wait_warp(sh, &sh.row_empty[buf], ((i / kJoinWarps) & 1) ^ 1)) return;
       for (int32_t v0 = 0; v0 < nvec; v0 += kStageVecs, ++it) {
         const uint32_t st = it % kStages;
-        if (!ring_wait(sh, &sh.full[st], (it / kStages) & 1)) return;
+        if (!ring_wait_warp(sh, &sh.full[st], (it / kStages) & 1)) return;
         const uint4* src = ring + st * kStageVecs + mtid;
         if (nvec - v0 >= kStageVecs) {
           uint4 v[kUnroll];
@@ -720,7 +730,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
       lm::unpack2(e2, e, hi);
       e += hi;
       const float to = reference(m, c);
-      raise_to(s, e, r, to);
+      move_by(s, e, r - to);
       if (nan) s = NAN;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -728,7 +738,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
         if (ENT) e += __shfl_xor_sync(0xffffffffu, e, o);
       }
       if (a.top_k > 0) sh.seg[buf][mtid] = order_key(nan ? NAN : own);
-      if (lane == 0) sh.stat[buf][mwarp] = Sums{m, to, s, e};
+      if (lane == 0) sh.stat[buf][mwarp] = make_float4(m, to, s, e);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh.row_full[buf]);
     }
@@ -763,44 +773,45 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
       const float given = tok >= 0 && tok < a.vocab ? load_f32(x + tok) : 0.f;
       const int32_t at = lane < head ? lane : (lane >= 16 && lane - 16 < a.vocab - tail0) ? tail0 + lane - 16 : -1;
       const float single = at >= 0 ? load_f32(x + at) : -INFINITY;
-      if (!ring_wait(sh, &sh.row_full[buf], i & 1)) {
+      if (!ring_wait_warp(sh, &sh.row_full[buf], i & 1)) {
         if (lane == 0 && a.flags) atomicOr(a.flags, DOBB_FLAG_TIMEOUT);
         return;
       }
-      Sums t{-INFINITY, -FLT_MAX, 0.f, 0.f};
-      if (lane < kFwdWarps) t = sh.stat[buf][lane];
-      const float m1 = fmaxf(t.m, single);
-      float m = m1;
+      float4 q = make_float4(-INFINITY, -kWide, 0.f, 0.f);
+      if (lane < kFwdWarps) q = sh.stat[buf][lane];
+      float m = fmaxf(q.x, single);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float to = reference(m, c);
-      if (fabsf(m) != INFINITY && fabsf(m * c) == INFINITY) {
-        t.s = t.e = 0.f;
+      Sums t{m, 0.f, 0.f};
+      if (is_wide(m, c)) {
+#pragma unroll 8
         for (int32_t j = lane; j < a.vocab; j += 32) {
           const float w = lm::max_nan((load_f32(x + j) - m) * c, -200.f), p = lm::exp2_fast(w);
           t.s += p;
           t.e += p * w;
         }
       } else {
-        raise_to(t.s, t.e, t.r, to);
+        const float to = reference(m, c);
         const float w = lm::max_nan(fmaf(single, c, -to), -200.f), p = lm::exp2_fast(w);
+        t.s = q.z;
+        t.e = q.w;
+        move_by(t.s, t.e, q.y - to);
         t.s += p;
         t.e += p * w;
+        move_to_max(t.s, t.e, to, m, c);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
         if (ENT) t.e += __shfl_xor_sync(0xffffffffu, t.e, o);
       }
-      t.m = m;
-      t.r = to;
       float log_sum = 0.f;
       if (lane == 0) log_sum = write_row<ENT>(a, row, t, tok, given);
       if (a.top_k > 0) {
         log_sum = __shfl_sync(0xffffffffu, log_sum, 0);
         const bool empty = m == -INFINITY && t.s == 0.f;
         slice_top<T, kFwdThreads, 1>(top, sh.seg[buf], x, a.vocab, 0, head, nvec, at, single, sh.pieces[buf],
-                        (nvec / kStageVecs / kPieces + 1) * kUnroll, a.top_k);
+                                     (nvec / kStageVecs / kPieces + 1) * kUnroll, a.top_k);
         if (lane < a.top_k) {
           const unsigned long long key = top.best[lane];
           a.top_ids[row * a.top_k + lane] = key_index(key);
@@ -913,8 +924,8 @@ dobb_status check_logits(const void* logits, int dtype, int64_t rows, int64_t vo
                 (long long)vocab);
   if (token_bytes != 4 && token_bytes != 8)
     return fail(DOBB_ERR_INVALID_ARG, "token_bytes must be 4 or 8 (got %d)", token_bytes);
-  if (!(scale > 0.f) || std::isinf(scale))
-    return fail(DOBB_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", scale);
+  if (!(scale > 0.f) || scale > 0x1p127f)  // scale log2(e) is finite, too
+    return fail(DOBB_ERR_INVALID_ARG, "scale must lie in (0, 2^127] (got %g)", scale);
   if (rows == 0) return DOBB_OK;
   if (!logits || !tokens) return fail(DOBB_ERR_INVALID_ARG, "logits and tokens must be non-NULL");
   if (lm::misaligned(logits, lm::dtype_bytes(dtype)) || lm::misaligned(tokens, token_bytes))

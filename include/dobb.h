@@ -377,7 +377,7 @@ const char* dobb_eigh_noalloc_last_error(void);
  * lse, logp, entropy and top_logp.  A token < 0 stands for none: logp 0.  A
  * token >= vocab has logp NaN and sets DOBB_FLAG_BAD_TOKEN.
  *   logits_dev  rows x vocab, row r at r * row_stride elements
- *   scale       > 0 and finite (the inverse temperature)
+ *   scale       in (0, 2^127] (the inverse temperature)
  *   top_k       0 ... min(DOBB_MAX_TOP_K, vocab)
  *   logp, lse, row_max, log_sum, entropy  rows floats each; entropy and lse
  *               may be NULL (not computed)

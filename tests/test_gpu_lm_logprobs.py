@@ -152,6 +152,38 @@ def test_masked_rows_lowest_values_and_non_finite(dtype, rows, vocab):
     assert_close(d[~bad], want[~bad], b[~bad] + HALF_UNIT[dtype] * np.abs(want[~bad]) * (1 + 1e-3) + TINY[dtype], "dlogits")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 9, 330])
+@pytest.mark.parametrize("vocab", [50, 20011])
+@pytest.mark.parametrize("scale", [1.0, 1.25])
+def test_finite_masks_and_huge_logits(dtype, rows, vocab, scale):
+    """Masks that are ordinary numbers, alone in a row and next to others, and
+    logits so large that their product with log2(e) rounds by more than one."""
+    rng = np.random.default_rng(vocab)
+    x = rng.standard_normal((rows, vocab)).astype(np.float32)
+    masks = [-1e9, -1e10, -1e30, -1.4e9, -1.6e9, 2.5e9, 7e20, -3e38]
+    for i in range(rows):
+        v = np.float32(masks[i % len(masks)])
+        kind = (i // len(masks) + i) % 3
+        if kind == 0:
+            x[i] = v                                     # nothing else
+        elif kind == 1:
+            x[i, : vocab - 1] = v                        # one entry is not masked
+        else:
+            x[i, rng.random(vocab) < 0.5] = v
+        if abs(v) < 1e11:
+            x[i, 3:9] *= np.float32(1 + 2.0 ** -20)      # neighbours, some units away
+    x = rounded(x, dtype)
+    t = rng.integers(0, vocab, rows)
+    xd, td, r = _forward(x, t, dtype, scale, 4)
+    f, eS, eH = _check_forward(x, t, r, float(np.float32(scale)), 4)
+    g = rng.standard_normal(rows).astype(np.float32)
+    d = np64(_dobb().log_probs_backward(xd, td, r, torch.from_numpy(g).cuda(), grad_entropy=torch.from_numpy(g).cuda()))
+    want = L.log_probs_backward(x, t, g, g, None, float(np.float32(scale)))
+    b = grad_bound(x, t, f, eS, eH, g, g, None, scale, dtype)
+    assert_close(d, want, b + HALF_UNIT[dtype] * np.abs(want) * (1 + 1e-3) + TINY[dtype], "dlogits")
+
+
 def test_tokens_outside_the_vocabulary_set_the_flag():
     x, _ = _logits(5, 300, 1, "f32")
     t = np.array([0, -1, 300, 7, 1 << 20])
