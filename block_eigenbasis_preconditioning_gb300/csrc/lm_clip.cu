@@ -12,6 +12,10 @@
 // chains, and adds the result to an fp32 pair (hi, lo) that loses nothing.
 // Where the sum leaves the range in which fp32 squares are exact enough (large,
 // tiny or non-finite entries), the thread sums its entries again in fp64.
+//
+// Bound by HBM: the GPT-2 XL gradients, fp32 to bf16, 15.5 GB with the second
+// read in 2.26 ms, the copy rate; sums alone 5.9 TB/s.  Scaling 8 entries a
+// thread, strided, instead of 4 side by side took 3.29 ms.
 #include "lm_common.cuh"
 
 namespace dobb {

@@ -88,7 +88,8 @@ struct EmbedArgs {
 };
 
 // 2^span lanes take kPackets packets each of one token's row: short rows share
-// a warp, long ones are split over several.
+// a warp, long ones are split over several.  Bound by HBM: 16384 rows of 4096,
+// fp32 to bf16, 42.6 us, 88 % of the copy rate on the distinct rows.
 template <typename W, typename O, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) embed_forward(const EmbedArgs a) {
   const int64_t group = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> a.span;
@@ -160,9 +161,11 @@ __global__ void __launch_bounds__(kThreads) embed_forward(const EmbedArgs a) {
 // the key `vocab` and end up last.
 //
 // A sort of a few thousand tokens is a chain of latencies (12 us for 8192) that
-// one cluster works off while the zeros of the gradient are written: the fill
-// kernel is launched before it and lets it start at once, and the sort ends
-// only when the fill has.
+// one cluster works off while the zeros of the gradient are written (24 us for
+// 161 MB): the fill kernel is launched before it and lets it start at once, and
+// the sort ends only when the fill has.  More SMs help the passes over the
+// items (32768 tokens: 4 CTAs of 1024 threads 57 us, 8 29 us, 16 of 512 17 us);
+// what is left are the barriers and the exchange of totals.
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kBatch = 4;  // items in flight per lane
@@ -224,7 +227,7 @@ __device__ void sort_part(const SortArgs& a, SortShared& sh, cg::cluster_group& 
       for (int u = 0; u < kBatch; ++u) {
         same[u] = 0;
         if (i0 + u * 32 >= hi) continue;  // the same for the whole warp
-        // one ballot per bit of the digit: match.any takes 80 cycles of the SM, this 10
+        // one ballot per bit of the digit (match.any instead: 29 us, not 27, for 32768 tokens)
         const uint32_t digit = (k[u] >> shift) & (bins - 1);
         same[u] = __ballot_sync(0xffffffffu, i0 + u * 32 + lane < hi);
 #pragma unroll
@@ -349,7 +352,10 @@ __global__ void __launch_bounds__(kThreads) fill_rows(const FillArgs a) {
 // the unit.  A run that continues in another unit leaves a partial sum in the
 // workspace: slot 0 of a unit for the run that came from the unit before,
 // slot 1 for the one that begins here and goes on.  join_runs adds those up in
-// a fixed order.
+// a fixed order.  Bound by latency, with as many rows in flight as registers
+// hold: 8192 rows of 1600 bf16 9 us, 32761 of 1601 added to fp32 rows 51 us.
+// Rings of shared memory per warp (cp.async or bulk copies) took 16 and 64 us:
+// more instructions a row, and the chain of rows a warp has is what it waits for.
 constexpr int kSumThreads = 128;
 constexpr int kSlab = 8 * kSumThreads;  // columns
 constexpr int kMaxUnit = 64;
@@ -458,7 +464,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
   }
 }
 
-// Rows anywhere: eight columns per thread, kSumThreads apart.
+// Rows anywhere: eight columns per thread, kSumThreads apart.  (Packets shifted
+// into place, with a shift per row: 183 instructions a packet, 105 us, not 51.)
 template <typename G, typename O, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) sum_runs_any(const SumArgs a) {
   constexpr int kRows = 2;  // in flight
@@ -580,7 +587,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a, int32
 }
 
 // Tokens per unit: long units leave fewer partial sums, short ones keep the
-// GPU busy when there are few tokens.
+// GPU busy when there are few tokens.  At least 3, 6 or 12 CTAs an SM for 8192
+// rows of 1600: sums 12.4, 9.6, 10.5 us, joins 6.2, 7.8, 11.2.
 int32_t unit_of(int64_t count, int64_t dim) {
   const int64_t slabs = (dim + kSlab - 1) / kSlab;
   int32_t unit = 4;
