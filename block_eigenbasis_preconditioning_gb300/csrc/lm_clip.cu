@@ -170,10 +170,10 @@ struct Entries {
   uint32_t w[kWords];
   __device__ __forceinline__ void load(const T* p) {
     if (kWords == 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 v = *reinterpret_cast<const uint4*>(p);  // in place, p is written later
       w[0] = v.x, w[1] = v.y, w[kWords - 2] = v.z, w[kWords - 1] = v.w;
     } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
       w[0] = v.x, w[1] = v.y;
     }
   }

@@ -130,11 +130,12 @@ __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
   return h < n ? h : n;
 }
 
+// (Plain loads: the callers may write the same tensor, each thread its own part.)
 // The 16 bytes at p, of which [floor16(p), floor16(p) + 32) may be read: two
 // aligned loads, shifted by the (warp-uniform) misalignment s = p mod 16 > 0.
 __device__ __forceinline__ uint4 load_shifted16(const void* p, uint32_t s) {
   const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - s);
-  const uint4 a = __ldg(q), b = __ldg(q + 1);
+  const uint4 a = q[0], b = q[1];
   uint32_t w[6] = {a.x, a.y, a.z, a.w, b.x, b.y};
   if (s & 8) {
     w[0] = a.z;
@@ -160,7 +161,7 @@ __device__ __forceinline__ uint4 load_shifted16(const void* p, uint32_t s) {
 template <typename T>
 __device__ __forceinline__ uint4 load16(const T* p, int64_t i, int64_t n, uint32_t s) {
   constexpr int N = 16 / (int)sizeof(T);
-  if (s == 0) return __ldg(reinterpret_cast<const uint4*>(p + i));
+  if (s == 0) return *reinterpret_cast<const uint4*>(p + i);
   const int64_t before = s / (uint32_t)sizeof(T);
   if (i >= before && i - before + 2 * N <= n) return load_shifted16(p + i, s);
   uint32_t w[4];
