@@ -527,27 +527,53 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs_any(const SumArgs a) {
 }
 
 // Runs over several units: the partial sums of the units, in interleaved
-// chains that are joined in order.
-constexpr int kJoinLanes = 64;   // of a CTA
-constexpr int kJoinPairs = 4;    // of columns per thread
+// chains that are joined in order.  A run of up to kShortRun units is joined by
+// the CTAs of the unit where it begins, each a slab of columns; of a longer one
+// the CTAs of its first kShortRun units take a share of each slab (one token
+// repeated, 1600 bf16 columns, whole gradient: 32768 tokens 48 us, 131072 tokens
+// 168 us; with the first unit's CTAs alone 96 us and 459 us).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinPairs = 4;  // short: pairs of columns per thread
+constexpr int kJoinRows = 4;   // chains
+constexpr int kJoinLanes = kJoinThreads / kJoinRows;
 constexpr int kJoinCols = 2 * kJoinLanes * kJoinPairs;
-constexpr int kJoinRows = 4;
-constexpr int kJoinThreads = kJoinLanes * kJoinRows;
+constexpr int kShortRun = 8;
+constexpr int kLongLanes = kJoinCols / kShortRun / 4;  // long: four columns per thread
+constexpr int kLongRows = kJoinThreads / kLongLanes;
+// the CTAs that find no run to join are the most: six to an SM (131072 uniform
+// tokens 201 us; 216 us with the three that the registers would allow)
+constexpr int kJoinCtas = 6;
 
 template <typename O, bool ADD>
-__global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a, int32_t slabs) {
-  __shared__ float2 red[kJoinRows][kJoinPairs][kJoinLanes];
+__device__ __forceinline__ void write_joined(const SumArgs& a, uint32_t v, int64_t col, float sum) {
+  if (col >= a.dim) return;
+  O* o = static_cast<O*>(a.out) + (int64_t)v * a.out_stride + col;
+  store_f32(o, ADD ? fmaf(sum, a.scale, load_f32(o)) : sum * a.scale);
+}
+
+template <typename O, bool ADD>
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtas) join_runs(const SumArgs a, int32_t slabs) {
+  __shared__ union {
+    float2 pair[kJoinRows][kJoinPairs][kJoinLanes];
+    float4 quad[kLongRows][kLongLanes];
+  } red;
   wait_for_previous();
   const int32_t u = blockIdx.x / (unsigned)slabs;
-  const int lane = threadIdx.x % kJoinLanes, row = threadIdx.x / kJoinLanes;
-  const int64_t col = (int64_t)(blockIdx.x % (unsigned)slabs) * kJoinCols + 2 * lane;
-  // does a run begin in unit u and go on in the next one?
+  const int64_t slab = (int64_t)(blockIdx.x % (unsigned)slabs) * kJoinCols;
+  // does a run go on from unit u into the next one?
   const int64_t lo = (int64_t)u * a.unit, hi = lo + a.unit;
   if (hi >= a.count) return;
-  const uint32_t v = a.item[hi - 1].x, next = a.item[hi].x, first = a.item[lo].x,
-                 before = lo > 0 ? a.item[lo - 1].x : kNoToken;
-  if (v >= (uint32_t)a.vocab || next != v || (first == v && before == v)) return;
+  const uint32_t v = a.item[hi - 1].x;
+  if (v >= (uint32_t)a.vocab || a.item[hi].x != v) return;
+  // how many units before it began, when this unit lies within it
+  int back = 0;
+  if (lo > 0 && a.item[lo].x == v && a.item[lo - 1].x == v) {
+    const int64_t j = ((int64_t)u - threadIdx.x) * a.unit - 1;
+    back = __syncthreads_count(threadIdx.x < kShortRun && j >= 0 && a.item[j].x == v);
+    if (back == kShortRun) return;
+  }
   // it reaches the units whose first token is v
+  const int32_t begin = u - back;
   int32_t last = u;
   for (int32_t at = u + 1;; at += kJoinThreads) {
     const int64_t j = ((int64_t)at + threadIdx.x) * a.unit;
@@ -555,35 +581,62 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a, int32
     last += reached;
     if (reached < kJoinThreads) break;
   }
-  float2 sum[kJoinPairs];
+  const bool is_short = last - begin < kShortRun;
+  if (is_short && back > 0) return;
+  // slot 1 of the unit where it begins, slot 0 of the others
+  auto part = [&](int32_t i) { return a.part + (2 * (int64_t)i + (i == begin)) * a.width; };
+  if (is_short) {
+    const int lane = threadIdx.x % kJoinLanes, row = threadIdx.x / kJoinLanes;
+    const int64_t col = slab + 2 * lane;
+    float2 sum[kJoinPairs];
 #pragma unroll
-  for (int k = 0; k < kJoinPairs; ++k) sum[k] = make_float2(0.f, 0.f);
-  for (int32_t i = u + row; i <= last; i += kJoinRows) {
-    const float* part = a.part + (2 * (int64_t)i + (i == u)) * a.width;
+    for (int k = 0; k < kJoinPairs; ++k) sum[k] = make_float2(0.f, 0.f);
+    for (int32_t i = begin + row; i <= last; i += kJoinRows) {
 #pragma unroll
-    for (int k = 0; k < kJoinPairs; ++k) {
-      if (col + 2 * kJoinLanes * k < a.dim) {
-        const float2 x = *reinterpret_cast<const float2*>(part + col + 2 * kJoinLanes * k);
-        sum[k].x += x.x;
-        sum[k].y += x.y;
+      for (int k = 0; k < kJoinPairs; ++k) {
+        if (col + 2 * kJoinLanes * k < a.dim) {
+          const float2 x = *reinterpret_cast<const float2*>(part(i) + col + 2 * kJoinLanes * k);
+          sum[k].x += x.x;
+          sum[k].y += x.y;
+        }
       }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < kJoinPairs; ++k) red[row][k][lane] = sum[k];
-  __syncthreads();
-  // row r of threads finishes pair r
-  static_assert(kJoinPairs == kJoinRows, "a row of threads per pair");
-  float2 t = red[0][row][lane];
+    for (int k = 0; k < kJoinPairs; ++k) red.pair[row][k][lane] = sum[k];
+    __syncthreads();
+    // row r of threads finishes pair r
+    static_assert(kJoinPairs == kJoinRows, "a row of threads per pair");
+    float2 t = red.pair[0][row][lane];
 #pragma unroll
-  for (int r = 1; r < kJoinRows; ++r) {
-    t.x += red[r][row][lane].x;
-    t.y += red[r][row][lane].y;
+    for (int r = 1; r < kJoinRows; ++r) {
+      t.x += red.pair[r][row][lane].x;
+      t.y += red.pair[r][row][lane].y;
+    }
+    write_joined<O, ADD>(a, v, col + 2 * kJoinLanes * row, t.x);
+    write_joined<O, ADD>(a, v, col + 2 * kJoinLanes * row + 1, t.y);
+  } else {
+    const int lane = threadIdx.x % kLongLanes, row = threadIdx.x / kLongLanes;
+    const int64_t col = slab + (back * kLongLanes + lane) * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < a.dim) {
+#pragma unroll 4
+      for (int32_t i = begin + row; i <= last; i += kLongRows) {
+        const float4 x = *reinterpret_cast<const float4*>(part(i) + col);
+        sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+      }
+    }
+    red.quad[row][lane] = sum;
+    __syncthreads();
+    if (row != 0) return;
+    for (int r = 1; r < kLongRows; ++r) {
+      const float4 x = red.quad[r][lane];
+      sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+    }
+    write_joined<O, ADD>(a, v, col, sum.x);
+    write_joined<O, ADD>(a, v, col + 1, sum.y);
+    write_joined<O, ADD>(a, v, col + 2, sum.z);
+    write_joined<O, ADD>(a, v, col + 3, sum.w);
   }
-  const int64_t c = col + 2 * kJoinLanes * row;
-  O* o = static_cast<O*>(a.out) + (int64_t)v * a.out_stride + c;
-  if (c < a.dim) store_f32(o, ADD ? fmaf(t.x, a.scale, load_f32(o)) : t.x * a.scale);
-  if (c + 1 < a.dim) store_f32(o + 1, ADD ? fmaf(t.y, a.scale, load_f32(o + 1)) : t.y * a.scale);
 }
 
 // Tokens per unit: long units leave fewer partial sums, short ones keep the

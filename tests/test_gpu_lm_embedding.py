@@ -127,6 +127,24 @@ def test_gradient_of_many_tokens(count, vocab, kind):
         assert torch.equal(got, _dobb().embedding_backward(gd, td, vocab, dtype=torch.float32))
 
 
+@pytest.mark.parametrize("gdt,odt", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("dim", [5, 512, 1601])
+def test_runs_of_every_length(gdt, odt, dim):
+    """Tokens that come 1, 2, 3 ... 90 times, then 700 times, in a shuffled
+    order: their runs begin at every offset within a unit of the sum and reach
+    over any number of units."""
+    c = np.concatenate([np.arange(1, 91), [700]])
+    rng = np.random.default_rng(dim + 1)
+    t = rng.permutation(np.repeat(np.arange(c.size), c))
+    grad = rounded(rng.standard_normal((t.size, dim)), gdt)
+    gd, td = dev(grad, gdt), torch.from_numpy(t).cuda()
+    before = rounded(rng.standard_normal((c.size, dim)), odt)
+    for add in (None, before):
+        out = dev(before, odt).clone()
+        _dobb().embedding_backward(gd, td, out=out, accumulate=add is not None)
+        _check_backward(grad, t, c.size, 1.0, gdt, odt, add, out)
+
+
 def test_gradient_against_differences():
     """<dout, embedding(W)> is linear in W: its difference quotient is exact,
     up to fp32 rounding of the lookups' products (2 u of each of 64 terms)."""
