@@ -32,8 +32,8 @@ MAX_TOP_K = 32
 
 class LogProbs(NamedTuple):
     """Result of `log_probs`, one entry per row (the alternatives: one row of
-    top_k).  stats, with the rows row_max and log_sum, and scale are what
-    `log_probs_backward` needs: lse = scale * row_max + log_sum."""
+    top_k).  stats, whose first two rows are row_max and log_sum, and scale are
+    what `log_probs_backward` needs: lse = scale * row_max + log_sum."""
     logp: torch.Tensor
     lse: torch.Tensor
     entropy: Optional[torch.Tensor]
@@ -65,6 +65,7 @@ class GradNorm(NamedTuple):
 # (0.1 us against 2 us); messages are built only when a check fails.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
@@ -102,7 +103,7 @@ class _On:
 
 
 def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]) -> bool:
-    return stream is not None or index != torch.cuda.current_device()
+    return stream is not None or index != _current_device()
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
@@ -187,7 +188,7 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
     check(load_library().dobb_log_probs(
         logits.data_ptr(), dtype, rows, vocab, stride, tokens.data_ptr(), token_bytes, scale, top_k, p + 2 * n, p + 3 * n, p,
         p + n, p + 4 * n if entropy else None, ids_p, alt_p, _flags(flags), _raw_stream(index)))
-    return LogProbs(f[2], f[3], f[4] if entropy else None, ids, alt, f[:2], float(scale))
+    return LogProbs(f[2], f[3], f[4] if entropy else None, ids, alt, f, float(scale))
 
 
 def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogProbs, grad_logp: torch.Tensor, *,
@@ -209,8 +210,10 @@ def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogPr
         with _On(index, stream, (logits, tokens, out, grad_logp, grad_entropy, grad_lse, result.stats,
                                  result.entropy)):
             return log_probs_backward(logits, tokens, result, grad_logp, grad_entropy=grad_entropy, grad_lse=grad_lse, out=out)
-    stats = _vector(result.stats, 2 * rows, "stats")
-    args = [stats, stats + 4 * rows,
+    stats = result.stats
+    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.dim() != 2 or stats.shape[0] < 2 or stats.shape[1] != rows:
+        raise ValueError(f"the result is not one for {rows} rows")
+    args = [stats.data_ptr(), stats.data_ptr() + 4 * rows,
             _vector(result.entropy if grad_entropy is not None else None, rows, "entropy"),
             _vector(grad_logp, rows, "grad_logp"), _vector(grad_entropy, rows, "grad_entropy"),
             _vector(grad_lse, rows, "grad_lse")]

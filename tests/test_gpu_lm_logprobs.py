@@ -281,3 +281,13 @@ def test_no_rows_other_stream_and_repeatability():
     for a, b in zip(r[:-1], q[:-1]):
         assert torch.equal(a, b)
     assert d.log_probs(xd, td, entropy=False).entropy is None
+
+
+def test_a_result_for_other_rows_is_refused():
+    d = _dobb()
+    xd, td, r = _forward(*_logits(3, 50, 1, "f32"), "f32", 1.0, 0)
+    g = torch.ones(2, device="cuda")
+    for bad in (r, r._replace(stats=r.stats[:1, :2].contiguous()), r._replace(stats=r.stats[:, :2]),
+                r._replace(stats=r.stats[:2, :2].double().contiguous())):
+        with pytest.raises(ValueError):
+            d.log_probs_backward(xd[:2], td[:2], bad, g)
