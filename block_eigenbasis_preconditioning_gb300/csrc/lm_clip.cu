@@ -8,21 +8,31 @@
 // them, in the same order: some KB from L2), and scales the stretches, last
 // chunk first: what the first kernel read last is still in L2.
 //
-// Within a chunk a thread sums the squares of its 32 entries in four fp32
+// Within a chunk a thread sums the squares of 32 of its entries in four fp32
 // chains, and adds the result to an fp32 pair (hi, lo) that loses nothing.
 // Where the sum leaves the range in which fp32 squares are exact enough (large,
 // tiny or non-finite entries), the thread sums its entries again in fp64.
 //
 // Bound by HBM: the GPT-2 XL gradients, fp32 to bf16, 15.5 GB with the second
-// read in 2.26 ms, the copy rate; sums alone 5.9 TB/s.  Scaling 8 entries a
-// thread, strided, instead of 4 side by side took 3.29 ms.
+// read in 2.25 ms, the copy rate; sums alone 5.9 TB/s.  Scaling 8 entries a
+// thread, strided, instead of 4 side by side took 3.29 ms.  Two CTAs an SM with
+// 64 entries a thread in flight instead of four with 32, and small tensors a
+// warp each instead of one after another: 12 layers of 768 with their vectors,
+// bf16, 62 to 35 us, fp32 to bf16 115 to 102; GPT-2 Small fp32 186 to 177.
 #include "lm_common.cuh"
 
 namespace dobb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;  // entries
+constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 2;     // per SM
+constexpr int kEach = 64;    // entries of a chunk per thread, in flight together
+constexpr int kSum = 32;     // of which so many are summed in plain fp32
+constexpr int kChunk = kEach * kThreads;
+// Neighbouring tensors of up to this many entries (biases, norms) are taken
+// together, a warp each: one after another each costs its latency.
+constexpr int kSmall = 4096;
 constexpr int kSms = 152;
 constexpr int kMaxTensors = 512;  // of a launch: the tables travel in the kernel parameters
 constexpr int kFewTensors = 32;   // a table of 1 KB, launched faster
@@ -80,53 +90,57 @@ struct Squares {
 // the smallest normal number) could show; zeros alone are exact.
 constexpr float kSmallest = 1.2e-35f;  // 2^-116
 
-template <typename T>
-__device__ __forceinline__ void add_chunk(Squares& sum, const T* p, int32_t n) {
+// n entries, up to kEach per thread of THREADS (tid: 0 ... THREADS - 1).
+template <int THREADS, typename T>
+__device__ __forceinline__ void add_chunk(Squares& sum, const T* p, int32_t n, int tid) {
   using V = lm::Vec16<T>;
-  constexpr int kVecs = kChunk / V::N / kThreads;
+  constexpr int kVecs = kEach / V::N;
   const int32_t head = (int32_t)lm::head_of(p, n), nvec = (n - head) / V::N, tail0 = head + nvec * V::N;
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
-  const int tid = threadIdx.x;
   // an entry before or behind the vectors: fewer than 8 each
-  const int32_t at = tid < head ? tid : (tid >= 32 && tid - 32 < n - tail0) ? tail0 + tid - 32 : -1;
+  const int32_t at = tid < head ? tid : (tid >= 8 && tid - 8 < n - tail0) ? tail0 + tid - 8 : -1;
   uint4 x[kVecs];
 #pragma unroll
   for (int u = 0; u < kVecs; ++u)
-    x[u] = tid + u * kThreads < nvec ? __ldg(v + tid + u * kThreads) : make_uint4(0, 0, 0, 0);
-  const float single = at >= 0 ? load_f32(p + at) : 0.f;
-  uint64_t s[2] = {0, 0};
-  uint32_t bits = 0;
+    x[u] = tid + u * THREADS < nvec ? __ldg(v + tid + u * THREADS) : make_uint4(0, 0, 0, 0);
+  float single = at >= 0 ? load_f32(p + at) : 0.f;
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    bits |= x[u].x | x[u].y | x[u].z | x[u].w;
+  for (int part = 0; part < kVecs; part += kSum / V::N) {
+    uint64_t s[2] = {0, 0};
+    uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < V::N / 2; ++i) {
-      const uint64_t w = V::pair(x[u], i);
-      s[i & 1] = lm::fma2(w, w, s[i & 1]);
-    }
-  }
-  float a, b, c, d;
-  lm::unpack2(s[0], a, b);
-  lm::unpack2(s[1], c, d);
-  const float t = fmaf(single, single, (a + b) + (c + d));
-  // (bits: the signs of zeros are no entries)
-  const bool zero = (bits & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) == 0 && single == 0.f;
-  if ((t >= kSmallest && t < INFINITY) || zero) {
-    sum.add(t);
-  } else {
-#pragma unroll 1
-    for (int32_t j = tid; j < nvec; j += kThreads)
-#pragma unroll 1
-      for (int i = 0; i < V::N; ++i) {
-        const double y = load_f32(p + head + j * V::N + i);
-        sum.wide += y * y;
+    for (int u = part; u < part + kSum / V::N; ++u) {
+      bits |= x[u].x | x[u].y | x[u].z | x[u].w;
+#pragma unroll
+      for (int i = 0; i < V::N / 2; ++i) {
+        const uint64_t w = V::pair(x[u], i);
+        s[i & 1] = lm::fma2(w, w, s[i & 1]);
       }
-    sum.wide += (double)single * single;
+    }
+    float a, b, c, d;
+    lm::unpack2(s[0], a, b);
+    lm::unpack2(s[1], c, d);
+    const float t = fmaf(single, single, (a + b) + (c + d));
+    // (bits: the signs of zeros are no entries)
+    const bool zero = (bits & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) == 0 && single == 0.f;
+    if ((t >= kSmallest && t < INFINITY) || zero) {
+      sum.add(t);
+    } else {
+#pragma unroll 1
+      for (int32_t j = tid + part * THREADS; j < min(nvec, (part + kSum / V::N) * THREADS); j += THREADS)
+#pragma unroll 1
+        for (int i = 0; i < V::N; ++i) {
+          const double y = load_f32(p + head + j * V::N + i);
+          sum.wide += y * y;
+        }
+      sum.wide += (double)single * single;
+    }
+    single = 0.f;
   }
 }
 
 template <int K>
-__global__ void __launch_bounds__(kThreads, 4) clip_sums(const __grid_constant__ Table<K> a, double* slots) {
+__global__ void __launch_bounds__(kThreads, kCtas) clip_sums(const __grid_constant__ Table<K> a, double* slots) {
   __shared__ double red[32];
   asm volatile("griddepcontrol.launch_dependents;");
   slots += a.slot0;
@@ -138,15 +152,33 @@ __global__ void __launch_bounds__(kThreads, 4) clip_sums(const __grid_constant__
   while (c < end) {
     Squares sum;
     const int32_t stop = min(end, a.chunk0[t + 1]);
+    int m = 0;  // small tensors side by side, empty ones among them
+    while (m < kWarps && t + m < a.num && a.numel[t + m] <= kSmall && a.chunk0[t + m + 1] <= end) ++m;
+    if (m > 1) {
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (warp < m) {
+        const int32_t n = (int32_t)a.numel[t + warp];
+        for (int32_t lo = 0; lo < n; lo += 32 * kEach) {
+          if (a.g_bf16[t + warp])
+            add_chunk<32>(sum, static_cast<const __nv_bfloat16*>(a.g[t + warp]) + lo, min(32 * kEach, n - lo), lane);
+          else
+            add_chunk<32>(sum, static_cast<const float*>(a.g[t + warp]) + lo, min(32 * kEach, n - lo), lane);
+        }
+        const double s = warp_sum_d((double)sum.hi + sum.lo + sum.wide);
+        if (lane == 0) slots[b + t + warp] = s;
+      }
+      t += m - 1;
+      c = a.chunk0[t + 1];
+    }
     for (; c < stop; ++c) {
       const int64_t lo = (int64_t)(c - a.chunk0[t]) * kChunk;
       const int32_t n = (int32_t)min((int64_t)kChunk, a.numel[t] - lo);
       if (a.g_bf16[t])
-        add_chunk(sum, static_cast<const __nv_bfloat16*>(a.g[t]) + lo, n);
+        add_chunk<kThreads>(sum, static_cast<const __nv_bfloat16*>(a.g[t]) + lo, n, threadIdx.x);
       else
-        add_chunk(sum, static_cast<const float*>(a.g[t]) + lo, n);
+        add_chunk<kThreads>(sum, static_cast<const float*>(a.g[t]) + lo, n, threadIdx.x);
     }
-    const double s = block_sum_d((double)sum.hi + sum.lo + sum.wide, red);
+    const double s = m > 1 ? 0.0 : block_sum_d((double)sum.hi + sum.lo + sum.wide, red);
     // the next slot that is written by this CTA or the next one
     int next = t;
     int32_t after = a.grid + a.num;
@@ -156,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_sums(const __grid_constant__
       if (c < a.chunk0[t + 1]) next = t;
       after = b + (c == end) + next;
     }
-    if (threadIdx.x == 0) slots[b + t] = s;
+    if (m <= 1 && threadIdx.x == 0) slots[b + t] = s;
     for (int i = b + t + 1 + threadIdx.x; i < after; i += kThreads) slots[i] = 0.0;
     t = next;
   }
@@ -200,21 +232,35 @@ struct Entries {
   }
 };
 
-// Input and output misaligned against each other (or at an end of a tensor).
-// Out of line: it would only push the common path out of the instruction cache.
-template <typename G, typename O>
-__device__ __noinline__ void scale_any(const G* p, O* o, int32_t n, float f) {
+// n entries by `threads` threads: a last chunk of a tensor, a small tensor, or
+// (value by value) one that is not on the vectors' boundaries.  Out of line:
+// it would only push the common path out of the instruction cache.
+template <typename G, typename O, int E>
+__device__ __noinline__ void scale_some(const G* p, O* o, int32_t n, float f, int tid, int threads) {
+  const uintptr_t off = (reinterpret_cast<uintptr_t>(p) % (E * sizeof(G))) |
+                        (reinterpret_cast<uintptr_t>(o) % (E * sizeof(O)));
+  const int32_t packed = off == 0 ? n / E * E : 0;
+  const uint64_t f2 = lm::pack2(f, f);
+#pragma unroll 4
+  for (int32_t j = tid * E; j < packed; j += threads * E) {
+    Entries<G, E> x;
+    x.load(p + j);
+    Entries<O, E> r;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) r.put(i, lm::mul2(x.pair(i), f2));
+    r.store(o + j);
+  }
 #pragma unroll 8
-  for (int32_t j = threadIdx.x; j < n; j += kThreads) store_f32(o + j, f * load_f32(p + j));
+  for (int32_t j = packed + tid; j < n; j += threads) store_f32(o + j, f * load_f32(p + j));
 }
 
 template <typename G, typename O>
-__device__ __forceinline__ void scale_chunk(const G* p, O* o, int32_t n, float f) {
+__device__ __forceinline__ void scale_chunk(const G* p, O* o, int32_t n, float f, int tid, int threads) {
   constexpr int E = sizeof(G) + sizeof(O) == 4 ? 8 : 4;
   constexpr int kTimes = kChunk / E / kThreads;
   const uintptr_t off = (reinterpret_cast<uintptr_t>(p) % (E * sizeof(G))) |
                         (reinterpret_cast<uintptr_t>(o) % (E * sizeof(O)));
-  if (off != 0 || n != kChunk) return scale_any(p, o, n, f);
+  if (off != 0 || n != kChunk || threads != kThreads) return scale_some<G, O, E>(p, o, n, f, tid, threads);
   const uint64_t f2 = lm::pack2(f, f);
   Entries<G, E> x[kTimes];
 #pragma unroll
@@ -230,7 +276,7 @@ __device__ __forceinline__ void scale_chunk(const G* p, O* o, int32_t n, float f
 
 // scale 0: the norms only
 template <int K>
-__global__ void __launch_bounds__(kThreads, 4) clip_scale(const __grid_constant__ Table<K> a, const double* slots,
+__global__ void __launch_bounds__(kThreads, kCtas) clip_scale(const __grid_constant__ Table<K> a, const double* slots,
                                                           int64_t num_slots, float max_norm, float* stats,
                                                           float* norms, uint32_t* flags, int scale) {
   __shared__ double red[32];
@@ -259,31 +305,45 @@ __global__ void __launch_bounds__(kThreads, 4) clip_scale(const __grid_constant_
   if (!scale) return;
   const int32_t b = blockIdx.x, first = first_chunk(a, b);
   int32_t c = first_chunk(a, b + 1) - 1;
+  // the n entries of tensor t from lo on
+  auto scale_part = [&](int t, int64_t lo, int32_t n, int tid, int threads) {
+    const float* gf = static_cast<const float*>(a.g[t]) + lo;
+    const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(a.g[t]) + lo;
+    float* of = static_cast<float*>(a.out[t]) + lo;
+    __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out[t]) + lo;
+    if (a.g_bf16[t]) {
+      if (a.out_bf16[t])
+        scale_chunk(gb, ob, n, f, tid, threads);
+      else
+        scale_chunk(gb, of, n, f, tid, threads);
+    } else if (a.out_bf16[t]) {
+      scale_chunk(gf, ob, n, f, tid, threads);
+    } else {
+      scale_chunk(gf, of, n, f, tid, threads);
+    }
+  };
+  const bool skip = f == 1.f;  // in place there is nothing to change
   for (int t = c >= first ? tensor_of(a, c) : 0; c >= first; --t) {
+    int m = 0;
+    while (m < kWarps && m <= t && a.numel[t - m] <= kSmall && a.chunk0[t - m] >= first) ++m;
+    if (m > 1) {
+      const int mine = t - (threadIdx.x >> 5);
+      if (mine > t - m && !(skip && a.out[mine] == a.g[mine]))
+        scale_part(mine, 0, (int32_t)a.numel[mine], lane, 32);
+      t -= m - 1;
+      c = a.chunk0[t] - 1;
+      continue;
+    }
     const int32_t stop = max(first, a.chunk0[t]);
-    if (f == 1.f && a.out[t] == a.g[t]) c = min(c, stop - 1);  // in place and nothing to change
+    if (skip && a.out[t] == a.g[t]) c = min(c, stop - 1);
     for (; c >= stop; --c) {
       const int64_t lo = (int64_t)(c - a.chunk0[t]) * kChunk;
-      const int32_t n = (int32_t)min((int64_t)kChunk, a.numel[t] - lo);
-      const float* gf = static_cast<const float*>(a.g[t]) + lo;
-      const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(a.g[t]) + lo;
-      float* of = static_cast<float*>(a.out[t]) + lo;
-      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out[t]) + lo;
-      if (a.g_bf16[t]) {
-        if (a.out_bf16[t])
-          scale_chunk(gb, ob, n, f);
-        else
-          scale_chunk(gb, of, n, f);
-      } else if (a.out_bf16[t]) {
-        scale_chunk(gf, ob, n, f);
-      } else {
-        scale_chunk(gf, of, n, f);
-      }
+      scale_part(t, lo, (int32_t)min((int64_t)kChunk, a.numel[t] - lo), threadIdx.x, kThreads);
     }
   }
 }
 
-int grid_of(int64_t chunks) { return (int)(chunks < 4 * kSms ? chunks : 4 * kSms); }
+int grid_of(int64_t chunks) { return (int)(chunks < kCtas * kSms ? chunks : kCtas * kSms); }
 
 // Slots of all launches; a launch takes up to kMaxTensors tensors.
 dobb_status measure(int num, const int64_t* numel, size_t* slots) {

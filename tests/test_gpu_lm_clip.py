@@ -72,6 +72,28 @@ def test_norm_and_clip(gdt, odt, which, offset):
     _check(xs, gds, gds, 0.25, r, gs)
 
 
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("count", [12, 400, 900])
+def test_small_tensors_side_by_side(seed, count):
+    """Small tensors, empty ones and longer ones in any order, types and
+    alignments: neighbours of up to a few thousand entries are taken together."""
+    rng = np.random.default_rng(1000 * seed + count)
+    sizes = rng.choice([0, 0, 1, 7, 8, 9, 768, 1024, 4095, 4096, 4097, 16384, 16385, 40000], count,
+                       p=[0.07] * 2 + [0.08] * 10 + [0.03] * 2)
+    gds, odts = rng.choice(["f32", "bf16"], (2, count))
+    xs = [rounded(rng.standard_normal(n) * 10.0 ** rng.uniform(-3, 1), d) for n, d in zip(sizes, gds)]
+    gs = [_view(x, d, int(o)) for x, d, o in zip(xs, gds, rng.integers(0, 5, count))]
+    outs = [_view(np.zeros(n), d, int(o)) for n, d, o in zip(sizes, odts, rng.integers(0, 5, count))]
+    r = _dobb().clip_grads(gs, 0.75, out=outs)
+    _check(xs, gds, odts, 0.75, r, outs)
+    r = _dobb().clip_grads(gs, 1e9, out=outs)
+    _check(xs, gds, odts, 1e9, r, outs)
+    q = _dobb().grad_norm(gs)
+    assert torch.equal(q.norms, r.norms) and torch.equal(q.norm, r.norm)
+    r = _dobb().clip_grads(gs, 0.75)
+    _check(xs, gds, gds, 0.75, r, gs)
+
+
 @pytest.mark.parametrize("gdt", ["f32", "bf16"])
 @pytest.mark.parametrize("size", [1e-30, 3e-23, 1e15, 2e19, 1e37])
 def test_squares_outside_the_range_of_fp32(gdt, size):
