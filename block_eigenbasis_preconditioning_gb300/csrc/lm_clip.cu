@@ -9,9 +9,10 @@
 // chunk first: what the first kernel read last is still in L2.
 //
 // Within a chunk a thread sums the squares of 32 of its entries in four fp32
-// chains, and adds the result to an fp32 pair (hi, lo) that loses nothing.
-// Where the sum leaves the range in which fp32 squares are exact enough (large,
-// tiny or non-finite entries), the thread sums its entries again in fp64.
+// chains, and adds the result to an fp32 pair (hi, lo) whose sum is exact but for
+// the rounding of lo.  Where the result lies outside [2^-116, 2^100) (large, tiny
+// or non-finite entries: fp32 squares are not exact enough, or the pair could
+// overflow on the way) the thread sums its entries again in fp64.
 //
 // Bound by HBM: the GPT-2 XL gradients, fp32 to bf16, 15.5 GB with the second
 // read in 2.25 ms, the copy rate; sums alone 5.9 TB/s.  Scaling 8 entries a
@@ -89,6 +90,9 @@ struct Squares {
 // Where 32 squares sum to less than this, their rounding (2^-150 each, below
 // the smallest normal number) could show; zeros alone are exact.
 constexpr float kSmallest = 1.2e-35f;  // 2^-116
+// A launch has fewer than 2^31 chunks, over 304 CTAs where there are as many: a
+// thread adds fewer than 2^24 sums to its pair, which stays below 2^124.
+constexpr float kLargest = 0x1p100f;
 
 // n entries, up to kEach per thread of THREADS (tid: 0 ... THREADS - 1).
 template <int THREADS, typename T>
@@ -123,7 +127,7 @@ __device__ __forceinline__ void add_chunk(Squares& sum, const T* p, int32_t n, i
     const float t = fmaf(single, single, (a + b) + (c + d));
     // (bits: the signs of zeros are no entries)
     const bool zero = (bits & (sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu)) == 0 && single == 0.f;
-    if ((t >= kSmallest && t < INFINITY) || zero) {
+    if ((t >= kSmallest && t < kLargest) || zero) {
       sum.add(t);
     } else {
 #pragma unroll 1
