@@ -278,6 +278,14 @@ __device__ __forceinline__ void scale_chunk(const G* p, O* o, int32_t n, float f
   }
 }
 
+// The same by a factor below the normal range of fp32, which fp32 would hold with
+// few bits or none (a norm of 1e39 brought to 1): each product in fp64, rounded to
+// fp32 and the output.
+template <typename G, typename O>
+__device__ __noinline__ void scale_tiny(const G* p, O* o, int32_t n, double c, int tid, int threads) {
+  for (int32_t j = tid; j < n; j += threads) store_f32(o + j, (float)(c * (double)load_f32(p + j)));
+}
+
 // scale 0: the norms only
 template <int K>
 __global__ void __launch_bounds__(kThreads, kCtas) clip_scale(const __grid_constant__ Table<K> a, const double* slots,
@@ -289,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_scale(const __grid_const
   for (int64_t i = threadIdx.x; i < num_slots; i += kThreads) sum += slots[i];
   const double norm = sqrt(block_sum_d(sum, red));
   const bool finite = isfinite(norm);
-  const float f = finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+  const double c64 = finite && norm > (double)max_norm ? (double)max_norm / norm : 1.0;
+  const float f = (float)c64;
+  const bool tiny = c64 < 0x1p-126 && c64 > 0.0;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     stats[0] = (float)norm;
     stats[1] = f;
@@ -311,19 +321,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_scale(const __grid_const
   int32_t c = first_chunk(a, b + 1) - 1;
   // the n entries of tensor t from lo on
   auto scale_part = [&](int t, int64_t lo, int32_t n, int tid, int threads) {
+    auto scaled = [&](auto* p, auto* o) {
+      if (tiny)
+        scale_tiny(p, o, n, c64, tid, threads);
+      else
+        scale_chunk(p, o, n, f, tid, threads);
+    };
     const float* gf = static_cast<const float*>(a.g[t]) + lo;
     const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(a.g[t]) + lo;
     float* of = static_cast<float*>(a.out[t]) + lo;
     __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out[t]) + lo;
     if (a.g_bf16[t]) {
       if (a.out_bf16[t])
-        scale_chunk(gb, ob, n, f, tid, threads);
+        scaled(gb, ob);
       else
-        scale_chunk(gb, of, n, f, tid, threads);
+        scaled(gb, of);
     } else if (a.out_bf16[t]) {
-      scale_chunk(gf, ob, n, f, tid, threads);
+      scaled(gf, ob);
     } else {
-      scale_chunk(gf, of, n, f, tid, threads);
+      scaled(gf, of);
     }
   };
   const bool skip = f == 1.f;  // in place there is nothing to change

@@ -451,8 +451,9 @@ size_t dobb_clip_grads_bytes(int num_tensors, const int64_t* numel);
  *   stats[1] = c = max_norm / norm if norm > max_norm, else 1
  *   out_i = c * G_i, rounded once to out_dtype[i]
  * stats_dev is 2 + num_tensors floats.  No square overflows or underflows on
- * the way: c is right wherever the norm is finite in 64 bits (a norm beyond
- * the fp32 range reads Inf in stats).  When an entry is NaN or Inf, norm is
+ * the way: c is right wherever the norm is finite in 64 bits, below the normal
+ * range of fp32, too (stats hold both rounded to fp32: a norm beyond its range
+ * reads Inf, a factor below it is a subnormal number or 0).  When an entry is NaN or Inf, norm is
  * NaN or Inf, DOBB_FLAG_NONFINITE_G is set and c = 1: the gradients are passed
  * on as they are, and the caller decides.
  *   G, out     host arrays of device pointers; `out` may be NULL (norms only,

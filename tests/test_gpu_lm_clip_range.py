@@ -10,16 +10,32 @@ more roundings and the output's."""
 import pytest
 import torch
 
-from lm_util import HALF_UNIT, TORCH, U
+from lm_util import HALF_UNIT, TINY, TORCH, U
 
 pytestmark = pytest.mark.gpu
 
 NORM = 8 * U
+FP32_MAX = float(torch.finfo(torch.float32).max)
 
 
 def _dobb():
     import block_eigenbasis_preconditioning_gb300 as d
     return d
+
+
+def _check(gs, max_norm, r, outs):
+    norms = torch.stack([g.double().square().sum().sqrt() for g in gs])
+    norm = float(norms.square().sum().sqrt())
+    c = max_norm / norm if norm > max_norm else 1.0
+    near = lambda got, want: got == float("inf") if want > FP32_MAX else abs(got - want) <= NORM * want + TINY["f32"]  # noqa: E731
+    assert near(float(r.norm), norm), (float(r.norm), norm)
+    assert abs(float(r.scale) - c) <= NORM * c + TINY["f32"]
+    assert all(near(float(a), float(b)) for a, b in zip(r.norms, norms))
+    for g, o in zip(gs, outs):
+        dt = "bf16" if o.dtype == torch.bfloat16 else "f32"
+        want = g.double() * c
+        bound = (NORM + 2 * U + HALF_UNIT[dt] * 1.001) * want.abs() + TINY[dt]
+        assert bool(((o.double() - want).abs() <= bound).all())
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -41,3 +57,16 @@ def test_squares_whose_sums_near_the_end_of_fp32(dtype, value, numel):
     entry = float(g[0]) / want
     assert float(outs[1].min()) == float(outs[1].max())
     assert abs(float(outs[1][0]) - entry) <= (NORM + 2 * U + HALF_UNIT[dtype] * 1.001) * entry
+
+
+@pytest.mark.parametrize("gdt,odt,in_place", [("f32", "f32", False), ("f32", "bf16", False), ("bf16", "f32", False), ("bf16", "bf16", False),
+                                              ("f32", "f32", True), ("bf16", "bf16", True)])
+@pytest.mark.parametrize("size,max_norm", [(1e37, 1e-3), (1e37, 1e-5), (3e38, 1e-7), (2e36, 7.0), (1e37, 1e-44)])
+def test_factors_below_the_normal_range_of_fp32(gdt, odt, in_place, size, max_norm):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    R = lambda *s: (torch.rand(*s, device="cuda", generator=gen) * 2 - 1) * size  # noqa: E731
+    gs = [R(300, 401).to(TORCH[gdt]), R(7).to(TORCH[gdt]), R(5).to(TORCH[gdt]), R(40001).to(TORCH[gdt])[1:]]
+    kept = [g.clone() for g in gs]
+    outs = gs if in_place else [torch.empty_like(g, dtype=TORCH[odt]) for g in gs]
+    r = _dobb().clip_grads(gs, max_norm, out=None if in_place else outs)
+    _check(kept, float(torch.tensor(max_norm)), r, outs)
