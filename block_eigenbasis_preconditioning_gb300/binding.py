@@ -81,6 +81,9 @@ SIGNATURES = [
     ("dobb_eigh_noalloc_last_error", _c.c_char_p, []),
     ("dobb_log_probs", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int,
                                   _c.c_float, _c.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    ("dobb_selftest_log_probs_timeout", _c.c_int,
+     [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int, _c.c_float, _c.c_int, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+      _VP, _c.c_int64, _c.c_uint64]),
     ("dobb_log_probs_backward", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP,
                                            _c.c_int, _c.c_float, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                            _c.c_int64, _VP]),

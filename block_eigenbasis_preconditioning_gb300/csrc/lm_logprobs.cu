@@ -640,19 +640,22 @@ constexpr int kRingBlocks = 3;  // per SM
 struct RingShared {
   uint64_t full[kStages], empty[kStages], row_full[kJoinWarps], row_empty[kJoinWarps];
   int32_t abort;
+  uint64_t wait_ns;  // the limit of a wait
   float4 stat[kJoinWarps][kFwdWarps];  // maximum, reference, and the sums relative to that
   uint32_t seg[kJoinWarps][kFwdThreads];  // key of every thread's maximum
   uint16_t pieces[kJoinWarps][kPieces * kFwdThreads];
   TopScratch top[kJoinWarps];
 };
 
-// Wait for a phase; false once a wait of this block has run out of time (2 s).
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Wait for a phase; false once a wait of this block has run out of time.
 __device__ __forceinline__ bool ring_wait(RingShared& sh, uint64_t* bar, uint32_t parity) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::global_timer_ns();
   while (!ptx::mbar_try_wait(bar, parity)) {
     if (*(volatile int32_t*)&sh.abort) return false;
-    if (ptx::global_timer_ns() - t0 > 2000000000ull) {
+    if (ptx::global_timer_ns() - t0 > sh.wait_ns) {
       *(volatile int32_t*)&sh.abort = 1;
       return false;
     }
@@ -665,8 +668,12 @@ __device__ __forceinline__ bool ring_wait_warp(RingShared& sh, uint64_t* bar, ui
   return __all_sync(0xffffffffu, ring_wait(sh, bar, parity));
 }
 
+// loaded: the rows that are copied in, all of them but in the self-test, where
+// the waits for the others run out.  A joining warp that gives up writes its
+// other rows as rows of NaN.
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(const LpArgs a, int64_t rows) {
+__global__ void __launch_bounds__(kRingThreads, kRingBlocks)
+    lp_forward_ring(const LpArgs a, int64_t rows, int64_t loaded, uint64_t wait_ns) {
   using V = lm::Vec16<T>;
   extern __shared__ __align__(128) unsigned char raw[];
   uint4* ring = reinterpret_cast<uint4*>(raw);
@@ -682,6 +689,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
       ptx::mbar_init(&sh.row_empty[s], 1);
     }
     sh.abort = 0;
+    sh.wait_ns = wait_ns;
     ptx::fence_mbar_init();
   }
   __syncthreads();
@@ -752,7 +760,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
   } else if (warp == kJoinWarps) {
     if (lane != 0) return;
     bool ok = true;
-    for (int64_t row = blockIdx.x; row < rows && ok; row += gridDim.x) {
+    for (int64_t row = blockIdx.x; row < loaded && ok; row += gridDim.x) {
       const T* x = logits + row * a.row_stride;
       const int32_t head = (int32_t)lm::head_of(x, a.vocab), nvec = (a.vocab - head) / V::N;
       const uint4* src = reinterpret_cast<const uint4*>(x + head);
@@ -770,6 +778,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
   } else {
     const int buf = warp;
     TopScratch& top = sh.top[buf];
+    bool ok = true;
     uint32_t i = 0;
     for (int64_t row = blockIdx.x + (int64_t)buf * gridDim.x; row < rows; row += (int64_t)kJoinWarps * gridDim.x, ++i) {
       const T* x = logits + row * a.row_stride;
@@ -780,13 +789,11 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
       const float given = tok >= 0 && tok < a.vocab ? load_f32(x + tok) : 0.f;
       const int32_t at = lane < head ? lane : (lane >= 16 && lane - 16 < a.vocab - tail0) ? tail0 + lane - 16 : -1;
       const float single = at >= 0 ? load_f32(x + at) : -INFINITY;
-      if (!ring_wait_warp(sh, &sh.row_full[buf], i & 1)) {
-        if (lane == 0 && a.flags) atomicOr(a.flags, DOBB_FLAG_TIMEOUT);
-        return;
-      }
+      ok = ok && ring_wait_warp(sh, &sh.row_full[buf], i & 1);  // not again once it has run out
+      if (!ok && lane == 0 && a.flags) atomicOr(a.flags, DOBB_FLAG_TIMEOUT);
       float4 q = make_float4(-INFINITY, -kWide, 0.f, 0.f);
       if (lane < kFwdWarps) q = sh.stat[buf][lane];
-      float m = fmaxf(q.x, single);
+      float m = ok ? fmaxf(q.x, single) : NAN;  // (NaN is wide, and stays)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       Sums t{m, 0.f, 0.f};
@@ -817,17 +824,18 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks) lp_forward_ring(con
       if (a.top_k > 0) {
         log_sum = __shfl_sync(0xffffffffu, log_sum, 0);
         const bool empty = m == -INFINITY && t.s == 0.f;
-        slice_top<T, kFwdThreads, 1>(top, sh.seg[buf], x, a.vocab, 0, head, nvec, at, single, sh.pieces[buf],
-                                     (nvec / kStageVecs / kPieces + 1) * kUnroll, a.top_k);
+        if (ok)
+          slice_top<T, kFwdThreads, 1>(top, sh.seg[buf], x, a.vocab, 0, head, nvec, at, single, sh.pieces[buf],
+                                       (nvec / kStageVecs / kPieces + 1) * kUnroll, a.top_k);
         if (lane < a.top_k) {
           const unsigned long long key = top.best[lane];
-          a.top_ids[row * a.top_k + lane] = key_index(key);
+          a.top_ids[row * a.top_k + lane] = ok ? key_index(key) : -1;
           a.top_logp[row * a.top_k + lane] =
               empty ? -INFINITY : a.scale * (key_value((uint32_t)(key >> 32)) - m) - log_sum;
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.row_empty[buf]);
+      if (ok && lane == 0) ptx::mbar_arrive(&sh.row_empty[buf]);
     }
   }
 }
@@ -941,14 +949,11 @@ dobb_status check_logits(const void* logits, int dtype, int64_t rows, int64_t vo
   return DOBB_OK;
 }
 
-}  // namespace
-
-extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtype, int64_t rows,
-                                      int64_t vocab, int64_t row_stride, const void* tokens,
-                                      int token_bytes, float scale, int top_k, float* logp,
-                                      float* lse, float* row_max, float* log_sum, float* entropy,
-                                      int32_t* top_ids, float* top_logp, uint32_t* flags,
-                                      void* stream) {
+// loaded, wait_ns: of the ring form; selftest: no other form will do
+dobb_status log_probs(const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                      const void* tokens, int token_bytes, float scale, int top_k, float* logp, float* lse,
+                      float* row_max, float* log_sum, float* entropy, int32_t* top_ids, float* top_logp,
+                      uint32_t* flags, void* stream, int64_t loaded, uint64_t wait_ns, bool selftest) {
   dobb_status st =
       check_logits(logits, logits_dtype, rows, vocab, row_stride, tokens, token_bytes, scale);
   if (st != DOBB_OK) return st;
@@ -979,7 +984,7 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
     auto launch = [&](auto kernel) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
-      kernel<<<grid, kRingThreads, smem, s>>>(a, rows);
+      kernel<<<grid, kRingThreads, smem, s>>>(a, rows, loaded, wait_ns);
       return cudaGetLastError();
     };
     cudaError_t e = logits_dtype == DOBB_F32
@@ -989,6 +994,7 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
     if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "log-probability launch: %s", cudaGetErrorString(e));
     return DOBB_OK;
   }
+  if (selftest) return fail(DOBB_ERR_UNSUPPORTED, "this call waits for no copies");
   int parts = 1;
   while (parts < kMaxCluster && rows * parts < kSms && vocab / parts > 4096) parts *= 2;
   const bool small = rows >= 4 * kSms && row_bytes < 8192;
@@ -1024,6 +1030,28 @@ extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtyp
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "log-probability launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
+}
+
+}  // namespace
+
+extern "C" dobb_status dobb_log_probs(const void* logits, dobb_dtype logits_dtype, int64_t rows,
+                                      int64_t vocab, int64_t row_stride, const void* tokens,
+                                      int token_bytes, float scale, int top_k, float* logp,
+                                      float* lse, float* row_max, float* log_sum, float* entropy,
+                                      int32_t* top_ids, float* top_logp, uint32_t* flags,
+                                      void* stream) {
+  return log_probs(logits, logits_dtype, rows, vocab, row_stride, tokens, token_bytes, scale, top_k, logp, lse, row_max,
+                   log_sum, entropy, top_ids, top_logp, flags, stream, rows, kWaitNs, false);
+}
+
+extern "C" dobb_status dobb_selftest_log_probs_timeout(
+    const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab, int64_t row_stride, const void* tokens,
+    int token_bytes, float scale, int top_k, float* logp, float* lse, float* row_max, float* log_sum, float* entropy,
+    int32_t* top_ids, float* top_logp, uint32_t* flags, void* stream, int64_t loaded_rows, uint64_t timeout_ns) {
+  if (loaded_rows < 0 || loaded_rows > rows || timeout_ns == 0 || timeout_ns > 5000000000ull)
+    return fail(DOBB_ERR_INVALID_ARG, "loaded_rows must lie in [0, rows], timeout_ns in [1, 5e9]");
+  return log_probs(logits, logits_dtype, rows, vocab, row_stride, tokens, token_bytes, scale, top_k, logp, lse, row_max,
+                   log_sum, entropy, top_ids, top_logp, flags, stream, loaded_rows, timeout_ns, true);
 }
 
 extern "C" dobb_status dobb_log_probs_backward(const void* logits, dobb_dtype logits_dtype,

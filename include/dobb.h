@@ -382,13 +382,31 @@ const char* dobb_eigh_noalloc_last_error(void);
  *   logp, lse, row_max, log_sum, entropy  rows floats each; entropy and lse
  *               may be NULL (not computed)
  *   top_ids, top_logp  rows x top_k, NULL when top_k is 0
- * rows may be 0 (nothing is done); vocab is 1 ... 2^31 - 1. */
+ * rows may be 0 (nothing is done); vocab is 1 ... 2^31 - 1.
+ * Many long rows are copied in ahead of the arithmetic, and the waits for those
+ * copies are bounded (2 s): a row that a wait gave up on reads as a row of NaN
+ * with NaN for row_max and -1 for top_ids, whether or not there are flags for
+ * DOBB_FLAG_TIMEOUT, and its gradient is NaN. */
 dobb_status dobb_log_probs(const void* logits_dev, dobb_dtype logits_dtype, int64_t rows,
                            int64_t vocab, int64_t row_stride, const void* tokens_dev,
                            int token_bytes, float scale, int top_k, float* logp_dev,
                            float* lse_dev, float* row_max_dev, float* log_sum_dev,
                            float* entropy_dev, int32_t* top_ids_dev, float* top_logp_dev,
                            uint32_t* flags_dev, void* stream);
+
+/* Self-test of those bounded waits: dobb_log_probs with a limit of timeout_ns
+ * (1 ns ... 5 s) and only the first loaded_rows rows copied in, so that the waits
+ * for the others run out.  Unlike the call itself it may leave earlier rows
+ * unfinished, too, where the limit is short.  DOBB_ERR_UNSUPPORTED for sizes that
+ * are computed without such waits. */
+dobb_status dobb_selftest_log_probs_timeout(const void* logits_dev, dobb_dtype logits_dtype,
+                                            int64_t rows, int64_t vocab, int64_t row_stride,
+                                            const void* tokens_dev, int token_bytes, float scale,
+                                            int top_k, float* logp_dev, float* lse_dev,
+                                            float* row_max_dev, float* log_sum_dev,
+                                            float* entropy_dev, int32_t* top_ids_dev,
+                                            float* top_logp_dev, uint32_t* flags_dev, void* stream,
+                                            int64_t loaded_rows, uint64_t timeout_ns);
 
 /* Gradient of dobb_log_probs with respect to the logits, for the gradients g
  * of logp, h of entropy and l of lse (rows floats each; h and l may be NULL,
