@@ -400,7 +400,8 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[
     `Dobb.step` takes).  When the norm is not finite the gradients are passed
     on unscaled and flag 2 (non-finite gradient) is set in `flags`.
 
-    grads: float32 or bfloat16 tensors, mixed if need be, of any shapes."""
+    grads: float32 or bfloat16 tensors, mixed if need be, of any shapes, none of
+    them listed twice: no output may share memory with another tensor."""
     if not max_norm >= 0:
         raise ValueError(f"max_norm must be >= 0, got {max_norm}")
     grads = list(grads)

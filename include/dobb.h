@@ -476,8 +476,9 @@ size_t dobb_clip_grads_bytes(int num_tensors, const int64_t* numel);
  * on as they are, and the caller decides.
  *   G, out     host arrays of device pointers; `out` may be NULL (norms only,
  *              max_norm is ignored and c = 1); out[i] may be G[i] (in place:
- *              nothing is written when c = 1) but must not overlap a tensor
- *              otherwise; an entry with numel 0 may be NULL
+ *              nothing is written when c = 1) but no output may share memory with
+ *              another gradient or output (refused; without `out` a tensor that
+ *              is listed twice counts twice); an entry with numel 0 may be NULL
  *   grad_dtype, out_dtype  host arrays of num_tensors dobb_dtype values
  *   numel      host array of entry counts (0 is allowed), dense tensors
  *   max_norm   >= 0, not NaN

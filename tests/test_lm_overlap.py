@@ -1,0 +1,78 @@
+"""Outputs that share memory with what the same call reads or writes elsewhere
+are refused before any device work (made-up addresses, no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+from block_eigenbasis_preconditioning_gb300 import binding
+
+P = 1 << 20        # a made-up device address
+FREE = 1 << 40     # another, far from all others
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if torch.cuda.is_available():
+        pytest.skip("a call that is not refused would run on made-up addresses")
+    return binding.load_library()
+
+
+def _refused(lib, st):
+    return st == 1 and b"overlap" in lib.dobb_last_error()
+
+
+def _clip(lib, g, gd, ne, out, od):
+    ptr = lambda v: (ctypes.c_void_p * len(v))(*v)  # noqa: E731
+    i32 = lambda v: (ctypes.c_int32 * len(v))(*v)  # noqa: E731
+    st = lib.dobb_clip_grads(len(g), ptr(g), i32(gd), (ctypes.c_int64 * len(ne))(*ne), 1.0, None if out is None else ptr(out),
+                             None if out is None else i32(od), FREE, None, FREE + (1 << 20), 1 << 20, None)
+    return _refused(lib, st)
+
+
+@pytest.mark.parametrize("g,gd,ne,out,od,refused", [
+    ((P, P), (0, 0), (16, 16), (P, P), (0, 0), True),                                  # a tied gradient, listed twice
+    ((P, P + 64), (0, 0), (16, 16), (P, P + 64), (0, 0), False),                       # neighbours, in place
+    ((P, P + 60), (0, 0), (16, 16), (P, P + 60), (0, 0), True),
+    ((P + 32, P), (1, 1), (16, 16), (P + 32, P), (1, 1), False),
+    ((P + 30, P), (1, 1), (16, 16), (P + 30, P), (1, 1), True),
+    ((P, P), (0, 0), (16, 16), (2 * P, 3 * P), (0, 0), False),                         # read twice
+    ((P, P), (0, 0), (16, 16), (P, 3 * P), (0, 0), True),                              # read by one, written by the other
+    ((P, 2 * P), (0, 0), (16, 16), (3 * P, 3 * P), (0, 0), True),                      # two outputs on one place
+    ((P, 2 * P), (0, 0), (16, 16), (2 * P, P), (0, 0), True),                          # exchanged
+    ((P, 2 * P), (0, 0), (16, 16), (P + 4, 3 * P), (0, 0), True),                      # over its own gradient, shifted
+    ((P, 2 * P), (0, 0), (16, 16), (P + 64, 3 * P), (1, 1), False),
+    ((P, 2 * P), (0, 1), (16, 16), (P + 60, 3 * P), (1, 1), True),
+    ((P, P, P + 8), (0, 0, 0), (16, 0, 0), (P, P, P + 4), (0, 0, 0), False),           # empty ones are nowhere
+    ((P, P + 4096, P + 64), (0, 0, 0), (1 << 20, 1, 1), (P, FREE, FREE + 8), (0, 0, 0), True),    # within a long one
+    ((P, P + 4096, 2 * P), (0, 0, 0), (16, 1 << 20, 4), (P, P + 4096, 2 * P), (0, 0, 0), True),
+    ((P, P), (0, 0), (16, 16), None, None, False)])                                    # norms only
+def test_clip(lib, g, gd, ne, out, od, refused):
+    assert _clip(lib, g, gd, ne, out, od) is refused
+
+
+def test_clip_of_many_tensors_in_any_order(lib):
+    gen = torch.Generator().manual_seed(1)
+    for n in (700, 40):
+        order = torch.randperm(n, generator=gen).tolist()
+        g = [P + 64 * i for i in order]
+        assert not _clip(lib, g, [0] * n, [16] * n, g, [0] * n)
+        assert not _clip(lib, g, [0] * n, [16] * n, [FREE + (1 << 30) + 32 * i for i in order], [1] * n)
+        bad = list(g)
+        bad[n // 2] = bad[n // 3]
+        assert _clip(lib, bad, [0] * n, [16] * n, bad, [0] * n)
+        assert _clip(lib, g, [0] * n, [16] * (n - 1) + [17 if order[-1] < n - 1 else 16], g, [0] * n) is (order[-1] < n - 1)
+
+
+@pytest.mark.gpu
+def test_a_gradient_listed_twice_is_refused():
+    import block_eigenbasis_preconditioning_gb300 as d
+    x, y = torch.ones(1000, device="cuda"), torch.ones(70, device="cuda")
+    for call in (lambda: d.clip_grads([x, y, x], 1.0), lambda: d.clip_grads([x[:600], x[500:]], 1.0),
+                 lambda: d.clip_grads([x, y], 1.0, out=[torch.empty_like(x), x[5:75]])):
+        with pytest.raises(binding.DobbError, match="overlap"):
+            call()
+    assert bool((x == 1).all())
+    assert abs(float(d.grad_norm([x, y, x]).norm) - 2070 ** 0.5) < 1e-4
+    d.clip_grads([x[:500], x[500:], y], 1.0)
+    assert abs(float(x.double().square().sum() + y.double().square().sum()) - 1.0) < 1e-5
