@@ -181,5 +181,32 @@ inline bool bad_dtype(int d) { return d != DOBB_F32 && d != DOBB_BF16; }
 inline bool misaligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 inline size_t dtype_bytes(int d) { return d == DOBB_F32 ? 4 : 2; }
 
+// A matrix in memory: `rows` rows of `width` bytes, `stride` bytes apart (width <= stride if rows > 1).
+struct RowExtent {
+  RowExtent(const void* p, int64_t rows, int64_t cols, int64_t stride, int dtype)
+      : at(reinterpret_cast<uintptr_t>(p)), rows(rows), width((uint64_t)cols * dtype_bytes(dtype)),
+        stride(rows > 1 ? (uint64_t)stride * dtype_bytes(dtype) : width) {}
+  uintptr_t at;
+  int64_t rows;
+  uint64_t width, stride;
+  uintptr_t end() const { return at + (uint64_t)(rows - 1) * stride + width; }
+};
+
+// Whether two matrices (rows, width > 0) share a byte: columns of one buffer
+// may lie side by side.
+inline bool rows_overlap(const RowExtent& x, const RowExtent& y) {
+  if (x.end() <= y.at || y.end() <= x.at) return false;
+  const RowExtent &a = x.rows <= y.rows ? x : y, &b = x.rows <= y.rows ? y : x;
+  // row i of a against the first row of b that ends behind its begin; with equal
+  // strides every row that meets b at all meets it as the first or the last does
+  const int64_t step = a.stride == b.stride && a.rows > 2 ? a.rows - 1 : 1;
+  for (int64_t i = 0; i < a.rows; i += step) {
+    const uintptr_t lo = a.at + (uint64_t)i * a.stride, hi = lo + a.width;
+    const uint64_t j = lo < b.at + b.width ? 0 : (lo - b.at - b.width) / b.stride + 1;
+    if (j < (uint64_t)b.rows && b.at + j * b.stride < hi) return true;
+  }
+  return false;
+}
+
 }  // namespace lm
 }  // namespace dobb

@@ -1076,6 +1076,10 @@ extern "C" dobb_status dobb_log_probs_backward(const void* logits, dobb_dtype lo
     return fail(DOBB_ERR_INVALID_ARG, "dlogits not aligned to its element size");
   if (dlogits == logits && out_stride != row_stride && rows > 1)
     return fail(DOBB_ERR_INVALID_ARG, "in place the strides must be equal");
+  // (blocks would read logits that others have written over)
+  if (dlogits != logits && lm::rows_overlap({logits, rows, vocab, row_stride, logits_dtype},
+                                            {dlogits, rows, vocab, out_stride, logits_dtype}))
+    return fail(DOBB_ERR_INVALID_ARG, "dlogits overlaps the logits without being them");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t per = (int64_t)kGradThreads * kGradVecs * (16 / (int64_t)lm::dtype_bytes(logits_dtype));
   const int64_t chunks = (vocab + per - 1) / per, most = ((int64_t)1 << 30) / chunks;

@@ -196,7 +196,8 @@ def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor, result: LogPr
                        out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Gradient with respect to the logits, given `log_probs`' result on the
     same logits and tokens and the gradients of logp, of the entropy and of
-    lse (float32, one per row).  `out` may be the logits themselves."""
+    lse (float32, one per row).  `out` may be the logits themselves, or share no
+    memory with them."""
     stride = _rows(logits, "logits")
     dtype = _float_dtype(logits.dtype, "logits")
     rows, vocab = logits.shape

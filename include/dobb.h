@@ -418,7 +418,7 @@ dobb_status dobb_selftest_log_probs_timeout(const void* logits_dev, dobb_dtype l
  * log_sum is NaN gets NaN.  row_max, log_sum and entropy are those of the
  * forward call with the same scale.  dlogits_dev has the logits' dtype, row r
  * at r * out_stride elements, and may be logits_dev itself (with the same
- * stride). */
+ * stride); any other overlap with the logits is refused. */
 dobb_status dobb_log_probs_backward(const void* logits_dev, dobb_dtype logits_dtype, int64_t rows,
                                     int64_t vocab, int64_t row_stride, const void* tokens_dev,
                                     int token_bytes, float scale, const float* row_max_dev,

@@ -76,3 +76,58 @@ def test_a_gradient_listed_twice_is_refused():
     assert abs(float(d.grad_norm([x, y, x]).norm) - 2070 ** 0.5) < 1e-4
     d.clip_grads([x[:500], x[500:], y], 1.0)
     assert abs(float(x.double().square().sum() + y.double().square().sum()) - 1.0) < 1e-5
+
+
+def _rows(at, rows, width, stride):
+    """The bytes of a matrix: the definition that the closed form is compared with."""
+    return {at + r * stride + c for r in range(rows) for c in range(width)}
+
+
+def _pairs(seed, count):
+    """Small matrices near each other: offset, rows, columns and strides, in elements."""
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=gen))  # noqa: E731
+    for _ in range(count):
+        cols = rnd(1, 6)
+        a, b = (cols + rnd(0, 9) for _ in range(2))
+        yield rnd(-60, 60), rnd(1, 7), rnd(1, 7), cols, a, a if rnd(0, 1) else b
+
+
+def _log_probs_backward(lib, at, rows, vocab, stride, ostride, dtype):
+    st = lib.dobb_log_probs_backward(P, dtype, rows, vocab, stride, FREE, 8, 1.0, FREE, FREE, None, FREE, None, None, at, ostride, None)
+    return _refused(lib, st)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_gradient_of_log_probabilities(lib, dtype):
+    b = 2 if dtype else 4
+    assert not _log_probs_backward(lib, P, 5, 8, 8, 8, dtype)               # in place
+    assert _log_probs_backward(lib, P + 8 * b, 5, 8, 8, 8, dtype)           # a row behind
+    assert not _log_probs_backward(lib, P + 40 * b, 5, 8, 8, 8, dtype)
+    assert not _log_probs_backward(lib, P + 8 * b, 8192, 8, 16, 16, dtype)  # halves of the same rows
+    assert _log_probs_backward(lib, P + 7 * b, 8192, 8, 16, 16, dtype) and _log_probs_backward(lib, P + 9 * b, 8192, 8, 16, 16, dtype)
+    assert _log_probs_backward(lib, P - 8000 * 16 * b, 8192, 8, 16, 16, dtype)
+    hits = 0
+    for off, rows, _, cols, s, t in _pairs(dtype, 3000):
+        if off == 0:
+            continue
+        want = bool(_rows(0, rows, cols, s) & _rows(off, rows, cols, t))
+        hits += want
+        assert _log_probs_backward(lib, P + off * b, rows, cols, s, t, dtype) is want, (off, rows, cols, s, t)
+    assert 300 < hits < 2700
+
+
+@pytest.mark.gpu
+def test_a_gradient_over_part_of_the_logits_is_refused():
+    import block_eigenbasis_preconditioning_gb300 as d
+    buf = torch.randn(70, 200, device="cuda")
+    t, g = torch.zeros(64, dtype=torch.int64, device="cuda"), torch.ones(64, device="cuda")
+    x = buf[:64, :100]
+    r = d.log_probs(x, t)
+    want, kept = d.log_probs_backward(x, t, r, g), x.clone()
+    for out in (buf[1:65, :100], buf[:64, 1:101], buf[3:67, 99:199]):
+        with pytest.raises(binding.DobbError, match="overlap"):
+            d.log_probs_backward(x, t, r, g, out=out)
+    assert torch.equal(x, kept)
+    assert torch.equal(d.log_probs_backward(x, t, r, g, out=buf[:64, 100:]), want) and torch.equal(x, kept)
+    assert torch.equal(d.log_probs_backward(x, t, r, g, out=x), want)
