@@ -702,6 +702,8 @@ extern "C" dobb_status dobb_embedding(const void* weight, dobb_dtype weight_dtyp
   if (lm::misaligned(weight, lm::dtype_bytes(weight_dtype)) ||
       lm::misaligned(out, lm::dtype_bytes(out_dtype)) || lm::misaligned(tokens, token_bytes))
     return fail(DOBB_ERR_INVALID_ARG, "weight, tokens or out not aligned to its element size");
+  if (lm::rows_overlap({weight, vocab, dim, weight_stride, weight_dtype}, {out, count, dim, out_stride, out_dtype}))
+    return fail(DOBB_ERR_INVALID_ARG, "out overlaps the weight");
   const bool aligned = rows_aligned(weight, weight_stride, lm::dtype_bytes(weight_dtype), out, out_stride,
                                     lm::dtype_bytes(out_dtype), dim);
   // lanes per row: enough for one packet each, at most a warp

@@ -237,7 +237,7 @@ def embedding(weight: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
     the weight's).  Tokens below 0 are padding and give zeros.
 
     weight: (vocab, dim) float32 or bfloat16 with contiguous rows; `out`: a
-    (tokens, dim) matrix with contiguous rows."""
+    (tokens, dim) matrix with contiguous rows, apart from the weight."""
     wstride = _rows(weight, "weight")
     wdtype = _float_dtype(weight.dtype, "weight")
     vocab, dim = weight.shape

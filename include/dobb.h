@@ -431,7 +431,8 @@ dobb_status dobb_log_probs_backward(const void* logits_dev, dobb_dtype logits_dt
  * fp32 and rounded once to out_dtype.  A token < 0 (padding) and a token >=
  * vocab give a row of zeros; the latter sets DOBB_FLAG_BAD_TOKEN.
  *   weight_dev  vocab x dim, row v at v * weight_stride elements
- *   out_dev     count x dim, row t at t * out_stride elements */
+ *   out_dev     count x dim, row t at t * out_stride elements; it shares no
+ *               memory with the weight (refused) */
 dobb_status dobb_embedding(const void* weight_dev, dobb_dtype weight_dtype, int64_t vocab,
                            int64_t dim, int64_t weight_stride, const void* tokens_dev,
                            int token_bytes, int64_t count, float scale, void* out_dev,

@@ -131,3 +131,34 @@ def test_a_gradient_over_part_of_the_logits_is_refused():
     assert torch.equal(x, kept)
     assert torch.equal(d.log_probs_backward(x, t, r, g, out=buf[:64, 100:]), want) and torch.equal(x, kept)
     assert torch.equal(d.log_probs_backward(x, t, r, g, out=x), want)
+
+
+def _check_matrices(call, dtype, seed):
+    """call(offset, rows there, rows at P, cols, stride there, stride at P) against the bytes."""
+    b, hits = 2 if dtype else 4, 0
+    for off, m, n, cols, s, t in _pairs(seed, 3000):
+        want = bool(_rows(off, m, cols, s) & _rows(0, n, cols, t))
+        hits += want
+        assert call(P + off * b, m, n, cols, s, t) is want, (off, m, n, cols, s, t)
+    assert 300 < hits < 2700
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_lookup(lib, dtype):
+    def call(at, count, vocab, dim, ostride, wstride):
+        return _refused(lib, lib.dobb_embedding(P, dtype, vocab, dim, wstride, FREE, 8, count, 1.0, at, dtype, ostride, None, None))
+    _check_matrices(call, dtype, 10 + dtype)
+    # 32-bit weights, 16-bit outputs
+    mixed = lambda at: _refused(lib, lib.dobb_embedding(P, 0, 100, 8, 8, FREE, 8, 4, 1.0, at, 1, 8, None, None))  # noqa: E731
+    assert mixed(P) and mixed(P + 3198) and not mixed(P + 3200) and mixed(P - 62) and not mixed(P - 64)
+
+
+@pytest.mark.gpu
+def test_a_lookup_into_the_weight_is_refused():
+    import block_eigenbasis_preconditioning_gb300 as d
+    w = torch.randn(50, 64, device="cuda")
+    t, kept = torch.arange(20, device="cuda"), w.clone()
+    for out in (w[:20], w[30:], w.view(100, 32)[:40].view(20, 64)):
+        with pytest.raises(binding.DobbError, match="overlap"):
+            d.embedding(w, t, out=out)
+    assert torch.equal(w, kept) and torch.equal(d.embedding(w[:30], t, out=w[30:]), kept[:20])
