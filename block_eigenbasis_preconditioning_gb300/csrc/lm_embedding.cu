@@ -772,6 +772,9 @@ extern "C" dobb_status dobb_embedding_backward(const void* grad, dobb_dtype grad
   if (ws_bytes < w.total)
     return fail(DOBB_ERR_STATE, "workspace of %zu bytes is smaller than the %zu required", ws_bytes,
                 w.total);
+  if (count > 0 && lm::rows_overlap({grad, count, dim, grad_stride, grad_dtype},
+                                    {dweight, vocab, dim, dweight_stride, dweight_dtype}))
+    return fail(DOBB_ERR_INVALID_ARG, "dweight overlaps the gradient");
   if (count == 0 && accumulate) return DOBB_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);

@@ -271,7 +271,7 @@ def embedding_backward(grad: torch.Tensor, tokens: torch.Tensor, vocab: Optional
     that do not occur are zero, or with `accumulate` stay as `out` has them.
 
     grad: tokens.shape + (dim,) contiguous, or a (tokens, dim) matrix with
-    contiguous rows; `out`: (vocab, dim) with contiguous rows."""
+    contiguous rows; `out`: (vocab, dim) with contiguous rows, apart from grad."""
     token_bytes = _token_bytes(tokens)
     count = tokens.numel()
     if grad.dim() < 1 or grad.numel() != count * grad.shape[-1]:

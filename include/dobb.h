@@ -453,7 +453,7 @@ size_t dobb_embedding_backward_bytes(int64_t count, int64_t vocab, int64_t dim);
  * rounded once.  Tokens outside [0, vocab) contribute nothing; those >= vocab
  * set DOBB_FLAG_BAD_TOKEN.  workspace_dev is caller memory of at least
  * dobb_embedding_backward_bytes(), 256-byte aligned; it holds nothing between
- * calls.  count is 0 ... 2^31 - 1, vocab 1 ... 2^30. */
+ * calls.  dweight shares no memory with grad (refused).  count is 0 ... 2^31 - 1, vocab 1 ... 2^30. */
 dobb_status dobb_embedding_backward(const void* grad_dev, dobb_dtype grad_dtype, int64_t count,
                                     int64_t dim, int64_t grad_stride, const void* tokens_dev,
                                     int token_bytes, int64_t vocab, float scale,

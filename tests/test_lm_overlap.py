@@ -162,3 +162,25 @@ def test_a_lookup_into_the_weight_is_refused():
         with pytest.raises(binding.DobbError, match="overlap"):
             d.embedding(w, t, out=out)
     assert torch.equal(w, kept) and torch.equal(d.embedding(w[:30], t, out=w[30:]), kept[:20])
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("accumulate", [0, 1])
+def test_gradient_of_the_lookup(lib, dtype, accumulate):
+    def call(at, vocab, count, dim, ostride, gstride):
+        return _refused(lib, lib.dobb_embedding_backward(P, dtype, count, dim, gstride, FREE, 8, vocab, 1.0, at, dtype, ostride,
+                                                         accumulate, None, FREE + (1 << 20), 1 << 30, None))
+    _check_matrices(call, dtype, 20 + dtype)
+
+
+@pytest.mark.gpu
+def test_a_gradient_into_itself_is_refused():
+    import block_eigenbasis_preconditioning_gb300 as d
+    g = torch.randn(50, 64, device="cuda")
+    t, kept = torch.arange(20, device="cuda"), g.clone()
+    for out in (g[:20], g[19:], g.view(100, 32)[9:39].view(15, 64)):
+        for add in (False, True):
+            with pytest.raises(binding.DobbError, match="overlap"):
+                d.embedding_backward(g[:20], t, out=out, accumulate=add)
+    assert torch.equal(g, kept)
+    assert torch.equal(d.embedding_backward(g[:20], t, out=g[20:]), torch.cat([kept[:20], torch.zeros(10, 64, device="cuda")]))
