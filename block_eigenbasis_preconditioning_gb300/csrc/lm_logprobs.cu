@@ -138,6 +138,12 @@ __device__ __forceinline__ bool is_wide(float m, float c) {
   return fabsf(m) != INFINITY && !(fabsf(m * c) < kWide);
 }
 
+// scale (x - m) for x <= m, where x - m may be beyond fp32 and the product not
+__device__ __forceinline__ float scaled_difference(float x, float m, float scale) {
+  const float d = x - m;
+  return d == -INFINITY ? 2.f * (scale * (0.5f * x - 0.5f * m)) : scale * d;
+}
+
 // the sums relative to a reference that is d larger (-d)
 __device__ __forceinline__ void move_by(float& s, float& e, float d) {
   d = lm::max_nan(d, -1000.f);
@@ -541,7 +547,7 @@ __device__ __forceinline__ float write_row(const LpArgs& a, int64_t row, const S
     lp = NAN;
     if (a.flags) atomicOr(a.flags, DOBB_FLAG_BAD_TOKEN);
   } else if (tok >= 0) {
-    lp = empty ? -INFINITY : a.scale * (given - r.m) - log_sum;
+    lp = empty ? -INFINITY : scaled_difference(given, r.m, a.scale) - log_sum;
   }
   a.logp[row] = lp;
   a.row_max[row] = r.m;
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
         r = Sums{m, 0.f, 0.f};
         for (int p = 0; p < parts; ++p) {
           Sums q = cluster.map_shared_rank(&sh, p)->part;
-          if (q.m != m) move_by(q.s, q.e, (q.m - m) * c);
+          if (q.m != m) move_by(q.s, q.e, scaled_difference(q.m, m, c));
           r.s += q.s;
           r.e += q.e;
         }
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
           const bool empty = sh.part.e != 0.f;
           a.top_ids[row * a.top_k + at] = key_index(mine);
           a.top_logp[row * a.top_k + at] =
-              empty ? -INFINITY : a.scale * (key_value((uint32_t)(mine >> 32)) - sh.part.m) - sh.part.s;
+              empty ? -INFINITY : scaled_difference(key_value((uint32_t)(mine >> 32)), sh.part.m, a.scale) - sh.part.s;
         }
       }
     }
@@ -831,7 +837,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks)
           const unsigned long long key = top.best[lane];
           a.top_ids[row * a.top_k + lane] = ok ? key_index(key) : -1;
           a.top_logp[row * a.top_k + lane] =
-              empty ? -INFINITY : a.scale * (key_value((uint32_t)(key >> 32)) - m) - log_sum;
+              empty ? -INFINITY : scaled_difference(key_value((uint32_t)(key >> 32)), m, a.scale) - log_sum;
         }
       }
       __syncwarp();
@@ -876,8 +882,10 @@ __global__ void __launch_bounds__(kGradThreads) lp_backward(const LpGradArgs a) 
   const float h = ENT ? a.scale * a.h[row] : 0.f;
   const float l = a.l ? a.scale * a.l[row] : 0.f;
   const float A = ENT ? l - g - h * a.entropy[row] : l - g, B = -h * kLn2;
-  const float c = a.scale * kLog2e, log2_sum = log_sum * kLog2e;
-  const uint64_t minus_m = lm::pack2(-m, -m), c2 = lm::pack2(c, c),
+  // x - m may be beyond fp32, and its product with a small scale not: half of both
+  const float half = fabsf(m) >= 0x1p100f && a.scale < 0.5f ? 0.5f : 1.f, minus_hm = -half * m;
+  const float c = a.scale * kLog2e / half, log2_sum = log_sum * kLog2e;
+  const uint64_t half2 = lm::pack2(half, half), minus_m = lm::pack2(minus_hm, minus_hm), c2 = lm::pack2(c, c),
                  minus_s = lm::pack2(-log2_sum, -log2_sum), A2 = lm::pack2(A, A), B2 = lm::pack2(B, B);
   const int32_t tok_vec = (tok >= head && tok < a.vocab) ? (int32_t)((tok - head) / V::N) : -1;
 #pragma unroll
@@ -888,7 +896,7 @@ __global__ void __launch_bounds__(kGradThreads) lp_backward(const LpGradArgs a) 
     if (!empty) {
 #pragma unroll
       for (int i = 0; i < V::N / 2; ++i) {
-        uint64_t w = lm::fma2(lm::add2(V::pair(v[u], i), minus_m), c2, minus_s);
+        uint64_t w = lm::fma2(lm::fma2(V::pair(v[u], i), half2, minus_m), c2, minus_s);
         float lo, hi;
         lm::unpack2(w, lo, hi);
         if (ENT) {  // p u is 0, not 0 * -inf, where p is 0
@@ -914,7 +922,7 @@ __global__ void __launch_bounds__(kGradThreads) lp_backward(const LpGradArgs a) 
     if (j >= 0) {
       float r = 0.f;
       if (!empty) {
-        const float w = lm::max_nan(fmaf(load_f32(x + j) - m, c, -log2_sum), -200.f);
+        const float w = lm::max_nan(fmaf(fmaf(load_f32(x + j), half, minus_hm), c, -log2_sum), -200.f);
         r = lm::exp2_fast(w) * fmaf(B, w, A) + (j == tok ? g : 0.f);
       }
       store_f32(d + j, r);
