@@ -53,7 +53,7 @@ struct Table {
   uint8_t g_bf16[K], out_bf16[K];
 };
 
-int64_t chunks_of(int64_t numel) { return (numel + kChunk - 1) / kChunk; }
+int64_t chunks_of(int64_t numel) { return numel / kChunk + (numel % kChunk != 0); }
 
 // Stretch of CTA b: chunks [first(b), first(b + 1)); the CTA of chunk c.
 template <int K>
