@@ -671,6 +671,11 @@ dobb_status check_grad_sizes(int64_t count, int64_t vocab, int64_t dim) {
   if (vocab < 1 || vocab > (1 << 30))
     return fail(DOBB_ERR_INVALID_ARG, "vocab must lie in [1, 2^30] (got %lld)", (long long)vocab);
   if (dim < 1) return fail(DOBB_ERR_INVALID_ARG, "dim must be >= 1 (got %lld)", (long long)dim);
+  // the joins have the largest grid; with that, all sizes and offsets fit 64 bits
+  const int64_t join_slabs = (dim - 1) / kJoinCols + 1;
+  const int64_t unit = join_slabs <= INT32_MAX ? unit_of(count, dim) : 1;
+  if (join_slabs > INT32_MAX || (count + unit - 1) / unit * join_slabs > INT32_MAX)
+    return fail(DOBB_ERR_UNSUPPORTED, "too many tokens times columns for one call");
   return DOBB_OK;
 }
 
@@ -707,7 +712,7 @@ extern "C" dobb_status dobb_embedding(const void* weight, dobb_dtype weight_dtyp
   const bool aligned = rows_aligned(weight, weight_stride, lm::dtype_bytes(weight_dtype), out, out_stride,
                                     lm::dtype_bytes(out_dtype), dim);
   // lanes per row: enough for one packet each, at most a warp
-  const int64_t packets = (dim + 7) / 8;
+  const int64_t packets = (dim - 1) / 8 + 1;
   int32_t span = 0;
   while (span < 5 && (1 << span) < packets) ++span;
   const int64_t per = (int64_t)kPackets << span, chunks = (packets + per - 1) / per;
@@ -838,8 +843,6 @@ extern "C" dobb_status dobb_embedding_backward(const void* grad, dobb_dtype grad
   a.unit = unit_of(count, dim);
   const int64_t slabs = (dim + kSlab - 1) / kSlab, join_slabs = (dim + kJoinCols - 1) / kJoinCols;
   const int64_t units = (count + a.unit - 1) / a.unit;
-  if (join_slabs > INT32_MAX || units * join_slabs > INT32_MAX)
-    return fail(DOBB_ERR_UNSUPPORTED, "too many tokens times columns for one call");
   a.slabs = (int32_t)slabs;
   auto sums = [&](auto writes, auto adds) {
     launch(true, accumulate ? adds : writes, (unsigned)(units * slabs), kSumThreads, 0, 1, a);
