@@ -70,3 +70,29 @@ def test_factors_below_the_normal_range_of_fp32(gdt, odt, in_place, size, max_no
     outs = gs if in_place else [torch.empty_like(g, dtype=TORCH[odt]) for g in gs]
     r = _dobb().clip_grads(gs, max_norm, out=None if in_place else outs)
     _check(kept, float(torch.tensor(max_norm)), r, outs)
+
+
+@pytest.mark.parametrize("gdt", ["f32", "bf16", "mixed"])
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+def test_many_chunks_per_block(gdt, odt):
+    """Tensors over many chunks and over several blocks' stretches, odd sizes
+    and offsets, with entries of very different size along the way."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    gs = []
+    for i, s in enumerate([(9001, 1601), (3,), (20000003,), (768,), (8000009,)]):
+        dt = TORCH[gdt if gdt != "mixed" else ("f32", "bf16")[i % 2]]
+        n = 1
+        for k in s:
+            n *= k
+        buf = torch.randn(n + i, device="cuda", generator=gen)
+        buf *= torch.exp(3.0 * torch.sin(torch.arange(n + i, device="cuda") * (6.0 / n)))
+        gs.append(buf.to(dt)[i:].view(s))
+    kept = [g.clone() for g in gs]
+    outs = [torch.empty(g.numel() + 1, device="cuda", dtype=TORCH[odt])[1:].view(g.shape) for g in gs]
+    for max_norm in (0.5, 1e9):
+        r = _dobb().clip_grads(gs, max_norm, out=outs)
+        _check(kept, max_norm, r, outs)
+        q = _dobb().clip_grads(gs, max_norm, out=outs)
+        assert torch.equal(r.norms, q.norms) and torch.equal(r.norm, q.norm)
+    r = _dobb().clip_grads(gs, 0.5)
+    _check(kept, 0.5, r, gs)
