@@ -11,7 +11,7 @@ namespace cg = cooperative_groups;
 // Where every row of both tensors starts on a 16-byte boundary and dim is a
 // multiple of eight, rows are worked on in packets of eight values.  Of other
 // rows (odd widths, odd strides) the lookup shifts the packets into place
-// (9000 rows of 1601 bf16: 15 us; value by value 25 us, bound by the number of
+// (9000 rows of 1601 bf16: 14 us; value by value 25 us, bound by the number of
 // requests).  The gradient sums them value by value, neighbouring lanes on
 // neighbouring values: every row of a run has a shift of its own, which cost
 // 183 instructions a packet (32761 rows of 1601: 105 us against 51).
@@ -530,8 +530,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs_any(const SumArgs a) {
 // chains that are joined in order.  A run of up to kShortRun units is joined by
 // the CTAs of the unit where it begins, each a slab of columns; of a longer one
 // the CTAs of its first kShortRun units take a share of each slab (one token
-// repeated, 1600 bf16 columns, whole gradient: 32768 tokens 48 us, 131072 tokens
-// 168 us; with the first unit's CTAs alone 96 us and 459 us).
+// repeated, 1600 bf16 columns, the whole call when it adds to what is there: 32768
+// tokens 48 us, 131072 tokens 167 us; with the first unit's CTAs alone 96 and 459).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinPairs = 4;  // short: pairs of columns per thread
 constexpr int kJoinRows = 4;   // chains

@@ -631,8 +631,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) lp_forward(const LpArgs a) {
 // at its own pace; three more warps, row about, join them, find the alternatives
 // and write the row while the eight are in the next ones.
 //
-// Bound by HBM without alternatives (8192 x 50257 bf16: 127 us with the entropy,
-// 120 without: the copy rate); with 5 alternatives 142 us, the issue slots 69 %
+// Bound by HBM without alternatives (8192 x 50257 bf16: 124 us with the entropy,
+// 119 without: the copy rate); with 5 alternatives 139 us, the issue slots 69 %
 // busy, with 20 155 us.  One block a row, without the ring: 191 us.  What was
 // tried, for 5 and 20 alternatives: 2 stages 144, 155; 2 blocks an SM with 4
 // joining warps 143, 151; 2 joining warps, and code for 4 loads at once in
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingBlocks)
 // In units of log 2, u_j = scale log2(e) (x_j - M) - log2(S):
 //   p_j = 2^{u_j},  dx_j = p_j (A + B u_j) + scale g [j = t]
 //   A = scale (l - g - h entropy),  B = -scale h ln 2
-// (B = 0 without h).  Bound by HBM: 8192 x 50257 bf16 245 us, 6.7 TB/s read and
+// (B = 0 without h).  Bound by HBM: 8192 x 50257 bf16 247 us, 6.7 TB/s read and
 // written.  One block takes kGradVecs vectors per thread of one
 // row, aligned to the output; the logits are shifted into place when the two
 // differ in alignment.  The rows go from the last to the first: a forward

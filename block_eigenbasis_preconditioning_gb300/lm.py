@@ -12,7 +12,13 @@ and the non-finite cases.  Results are new tensors unless `out` is given.
 Every call is asynchronous on `stream` (default: the current stream of the
 tensors' device); results and workspaces are allocated on that stream, and
 tensors that were made on another one are kept alive until it has passed.
-Wrong arguments raise ValueError before anything is launched.
+Arguments of the wrong kind, shape or place raise ValueError, values and
+overlaps that the library refuses (a scale of 0, an empty vocabulary, a gradient
+listed twice) raise DobbError, both before anything is launched.
+
+Autograd does not see these calls: results are not part of its graph, and what
+is written in place or into `out` does not raise a tensor's version.  The
+gradients are calls of their own.
 """
 from __future__ import annotations
 
