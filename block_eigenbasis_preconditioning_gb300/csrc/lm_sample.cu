@@ -64,6 +64,7 @@ constexpr int kFastK = 1024;      // the largest top_k that is found through the
 constexpr int kPieces = 8;        // parts of a thread's entries that have a maximum of their own
 constexpr int kBatch = 4;         // vectors of a thread in flight
 constexpr float kNear = 65536.f;  // |log2 e^{max y}| from which a row takes the general way
+constexpr float kFar = 0x1p100f;  // and |max|: a difference from it may leave fp32, its product with a small scale not
 
 struct Cut {
   uint32_t key;
@@ -149,8 +150,9 @@ struct Row {
   int shift;
   const float* noise;
   __device__ __forceinline__ float exponent(float x) const { return fmaf(x, half, minus_hm) * c; }
-  // the same where |max c| is below kNear (an entry far below gives -inf)
+  // the same in rows near zero (a product beyond fp32 gives -inf)
   __device__ __forceinline__ float near_exponent(float x) const { return (x - m) * c; }
+  static __device__ __forceinline__ bool near_zero(float m, float c) { return fabsf(m * c) < kNear && fabsf(m) < kFar; }
   __device__ __forceinline__ unsigned long long mass(float x) const {
     return (unsigned long long)__float2ull_rn(ldexpf(lm::exp2_fast(exponent(x)), shift));
   }
@@ -272,7 +274,7 @@ __device__ __forceinline__ float min_p_logit(float m, float scale, float min_p) 
 //
 // One block, any settings and numbers, every pass over the row in memory.  It
 // takes the rows that the ways below leave: a top_k above kFastK, more equal or
-// nearly equal logits at a border than the list holds, |scale max| beyond 2^16, two
+// nearly equal logits at a border than the list holds, |scale max| beyond 2^16 or |max| beyond 2^100, two
 // close candidates in one thread, random numbers that leave no candidate.
 // f(logit, index) of the row's entries, each thread's eight at a time loaded first (one
 // after the other: 509 x 50257 bf16 with top_k 2000 334 us against 317).
@@ -1113,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
     if (rank != 0) return;
     const int n = sh.nlist;
     r.m = m;
-    if (fast && n <= kList && fabsf(m * r.c) < kNear) {
+    if (fast && n <= kList && Row::near_zero(m, r.c)) {
       unsigned long long cut = n > top_k ? list_border(sh, n, top_k, 0, r, low, m, a.vocab) : 0;
       if (top_p < 1.f) {
         // the mass of the first k, then the border within them
@@ -1270,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
     for (int p = 0; p < parts; ++p) total += sh.sum[p] * lm::exp2_fast(fmaxf(sh.ref[p] - row_ref, -1000.f));
     total *= lm::exp2_fast(-fmaf(m, r.c, -row_ref));  // relative to m c itself
     r.m = m;
-    general = !(fabsf(m * r.c) < kNear);
+    general = !Row::near_zero(m, r.c);
     // the first block joins the candidates; false: the general way has to
     const auto decide = [&](const Part& listed, Pair kept) {
       Part q = listed;
