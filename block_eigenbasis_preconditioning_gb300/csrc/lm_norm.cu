@@ -235,10 +235,10 @@ extern "C" dobb_status dobb_layer_norm(const void* x, dobb_dtype x_dtype, int64_
   ext.write("mean", mean, 1, rows, rows, DOBB_F32);
   ext.write("rstd", rstd, 1, rows, rows, DOBB_F32);
   if ((st = ext.check()) != DOBB_OK) return st;
-  const Plan p = plan(rows, dim, false);
-  NormArgs a{x,   rows,       x_stride, (int32_t)dim, weight, bias, param_dtype == DOBB_BF16, eps,
-             out, out_stride, mean,     rstd,         p.shape, {}};
-  if (!p.wide) a.ring = ring_of(p, rows, dim, x_stride, x_dtype, 0, 0, false);
+  Plan p = plan(rows, dim, false);
+  const Ring ring = p.wide ? Ring{} : forward_ring(p, rows, dim, x_stride, x_dtype);
+  const NormArgs a{x,   rows,       x_stride, (int32_t)dim, weight, bias, param_dtype == DOBB_BF16, eps,
+                   out, out_stride, mean,     rstd,         p.shape, ring};
   const bool aligned = dim % 4 == 0 && aligned_rows(x, x_stride, x_dtype, rows) && aligned_rows(out, out_stride, out_dtype, rows);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
@@ -247,4 +247,17 @@ extern "C" dobb_status dobb_layer_norm(const void* x, dobb_dtype x_dtype, int64_
                       : (out_dtype == DOBB_F32 ? launch_forward<bf16, float>(a, p, aligned, s) : launch_forward<bf16, bf16>(a, p, aligned, s));
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "layer norm launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
+}
+
+extern "C" int64_t dobb_selftest_layer_norm_smem(int64_t rows, int64_t dim, dobb_dtype x_dtype, int64_t x_stride, dobb_dtype grad_dtype,
+                                                 int64_t grad_stride, int backward, int64_t* most) {
+  if (most) *most = lm::kMostSmem;
+  if (check_norm(rows, dim, x_dtype, x_stride, grad_dtype, grad_stride, DOBB_F32) != DOBB_OK || rows < 1) return -1;
+  Plan p = plan(rows, dim, backward != 0);
+  if (p.wide) return 0;
+  if (!backward) {
+    const Ring r = forward_ring(p, rows, dim, x_stride, x_dtype);
+    return (int64_t)ring_smem(p, r, false, false);
+  }
+  return (int64_t)ring_smem(p, ring_of(p, rows, dim, x_stride, x_dtype, grad_stride, grad_dtype, true), true, true);
 }

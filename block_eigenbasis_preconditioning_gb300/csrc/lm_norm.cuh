@@ -291,6 +291,13 @@ struct Plan {
 
 inline int rows_at_once(const Shape& s) { return s.groups * (32 / s.lanes); }
 
+// the rows over the blocks
+void spread(Plan& p, int64_t rows) {
+  const int64_t at_once = rows_at_once(p.shape);
+  p.blocks = (unsigned)std::min<int64_t>((rows + at_once - 1) / at_once, kSms);
+  p.partials = (int32_t)p.blocks;
+}
+
 Plan plan(int64_t rows, int64_t dim, bool backward) {
   Plan r{};
   r.wide = dim > (backward ? kMaxDim : kMaxForwardDim);
@@ -315,9 +322,7 @@ Plan plan(int64_t rows, int64_t dim, bool backward) {
   // few rows: a block for each
   const int64_t per_sm = (rows + kSms - 1) / kSms, in_warp = 32 / r.shape.lanes;
   r.shape.groups = (int)std::min<int64_t>(kWarps / r.shape.warps, (per_sm + in_warp - 1) / in_warp);
-  const int64_t at_once = rows_at_once(r.shape);
-  r.blocks = (unsigned)std::min<int64_t>((rows + at_once - 1) / at_once, kSms);
-  r.partials = (int32_t)r.blocks;
+  spread(r, rows);
   return r;
 }
 
@@ -345,6 +350,18 @@ Ring ring_of(const Plan& p, int64_t rows, int64_t dim, int64_t x_stride, int x_d
 // the parameters and the ring, and in their place at the end the sums of the groups
 size_t ring_smem(const Plan& p, const Ring& r, bool backward, bool sums) {
   return std::max((size_t)r.first + (size_t)r.slots * r.slot_bytes * (backward ? 1 : p.shape.groups), sums ? (size_t)p.shape.warps * p.shape.groups * 32 * 8 * p.p * 4 : 0);
+}
+
+// The forward pass's: one group less where a slot for each does not fit (fp32 rows of 14333 to
+// 14336 columns, parameters and two rows; the backward pass's shapes all fit).
+Ring forward_ring(Plan& p, int64_t rows, int64_t dim, int64_t x_stride, int x_dtype) {
+  Ring r = ring_of(p, rows, dim, x_stride, x_dtype, 0, 0, false);
+  while (ring_smem(p, r, false, false) > (size_t)lm::kMostSmem && p.shape.groups > 1) {
+    --p.shape.groups;
+    spread(p, rows);
+    r = ring_of(p, rows, dim, x_stride, x_dtype, 0, 0, false);
+  }
+  return r;
 }
 
 dobb_status check_norm(int64_t rows, int64_t dim, int x_dtype, int64_t x_stride, int other_dtype, int64_t other_stride,

@@ -533,6 +533,14 @@ dobb_status dobb_layer_norm_backward(const void* grad_dev, dobb_dtype grad_dtype
                                      dobb_dtype dparam_dtype, int accumulate, void* workspace_dev,
                                      size_t workspace_bytes, void* stream);
 
+/* Self-test: the dynamic shared memory in bytes that a layer norm call (backward 0)
+ * or its gradients (1) launch with, 0 where they go over the rows in memory, -1
+ * for sizes that are refused; *most (may be NULL): the largest that a launch may ask
+ * for.  No GPU is needed. */
+int64_t dobb_selftest_layer_norm_smem(int64_t rows, int64_t dim, dobb_dtype x_dtype, int64_t x_stride,
+                                      dobb_dtype grad_dtype, int64_t grad_stride, int backward,
+                                      int64_t* most);
+
 /* Largest number of a teacher's entries per row. */
 #define DOBB_MAX_TEACHER 256
 
