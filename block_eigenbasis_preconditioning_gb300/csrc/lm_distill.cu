@@ -372,14 +372,17 @@ struct Stretch {  // of one row
   using V = lm::Vec16<T>;
   const T* x;
   T* d;
-  int32_t head, nvec, tail0, stages;
+  int32_t head, nvec, tail0;
+  int32_t stages;  // the same for every row, whatever its alignment: the last may be without a vector
   __device__ __forceinline__ Stretch(const DistillArgs& a, int64_t row, int32_t lo, int32_t n) {
     x = static_cast<const T*>(a.logits) + row * a.row_stride + lo;
     d = static_cast<T*>(a.out) + row * a.out_stride + lo;
     head = (int32_t)lm::head_of(x, n);
     nvec = (n - head) / V::N;
     tail0 = head + nvec * V::N;
-    stages = (nvec + kStageVecs - 1) / kStageVecs;
+    // (with fewer in a row that starts later, its entries behind the vectors would lie in a
+    // stage for which the next row's copy waits for none of this row's readers)
+    stages = (n / V::N + kStageVecs - 1) / kStageVecs;
   }
 };
 
@@ -424,9 +427,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
       for (int s = 0; s < kMaxStages; ++s) {
         if (s >= r.stages || !ok) break;
         if (issued[s] > 0 && !(ok = row_wait(sh, &sh.empty[s], (issued[s] - 1) & 1, limit))) break;
-        const uint32_t bytes = (uint32_t)min(r.nvec - s * kStageVecs, kStageVecs) * 16;
-        ptx::mbar_arrive_expect_tx(&sh.full[s], bytes);
-        ptx::bulk_load(xv + s * kStageVecs, r.x + r.head + (int64_t)s * kStageVecs * V::N, bytes, &sh.full[s]);
+        const uint32_t bytes = (uint32_t)max(min(r.nvec - s * kStageVecs, kStageVecs), 0) * 16;
+        if (bytes > 0) {
+          ptx::mbar_arrive_expect_tx(&sh.full[s], bytes);
+          ptx::bulk_load(xv + s * kStageVecs, r.x + r.head + (int64_t)s * kStageVecs * V::N, bytes, &sh.full[s]);
+        } else {
+          ptx::mbar_arrive(&sh.full[s]);
+        }
         ++issued[s];
       }
     }
@@ -589,9 +596,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
       }
       __stcs(dv + j, o);
     };
-    const int32_t dstages = max(r.stages, (dvec + kStageVecs - 1) / kStageVecs);
 #pragma unroll 1
-    for (int st = 0; st < dstages; ++st) {
+    for (int st = 0; st < r.stages; ++st) {
       const int32_t v0 = st * kStageVecs + tid;
       if (shift == 0) {
         const uint4* src = reinterpret_cast<const uint4*>(xs + dhead);
@@ -609,8 +615,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
       // free when the next one has been read
       __syncwarp();
       if (lane == 0) {
-        if (st > 0 && st - 1 < r.stages) ptx::mbar_arrive(&sh.empty[st - 1]);
-        if (st == dstages - 1 && st < r.stages) ptx::mbar_arrive(&sh.empty[st]);
+        if (st > 0) ptx::mbar_arrive(&sh.empty[st - 1]);
+        if (st == r.stages - 1) ptx::mbar_arrive(&sh.empty[st]);
       }
     }
     __syncwarp();
