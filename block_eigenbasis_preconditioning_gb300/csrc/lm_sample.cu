@@ -156,6 +156,11 @@ struct Row {
   __device__ __forceinline__ unsigned long long mass(float x) const {
     return (unsigned long long)__float2ull_rn(ldexpf(lm::exp2_fast(exponent(x)), shift));
   }
+  // log2(e^{y - max}) - log2 E.  A random number of 0 wins, whatever the exponent (it may be
+  // -inf, and -inf + inf no number); NaN and negative ones lose.
+  static __device__ __forceinline__ float score(float exponent, float e) {
+    return e > 0.f ? exponent - __log2f(e) : e == 0.f ? INFINITY : -INFINITY;
+  }
   // y - log E relative to a reference logit, in 64 bits (as slow as 100 fp32
   // entries: only for what fp32 leaves open)
   static __device__ __noinline__ double exact(float x, float e, float scale, float ref) {
@@ -434,10 +439,7 @@ __device__ __noinline__ void sample_generic(SampleShared& sh, const SampleArgs& 
   if (top_p < 1.f) find_cut(sh, x, a.vocab, r, cut, 0, top_p);
   const uint32_t key = order_key(min_p_logit(r.m, r.scale, min_p));
   if (key > cut.key) cut = Cut{key, INT32_MAX};
-  const auto score = [&](float v, int32_t j) {
-    const float e = r.noise[j];
-    return e >= 0.f ? r.exponent(v) - __log2f(e) : -INFINITY;
-  };
+  const auto score = [&](float v, int32_t j) { return Row::score(r.exponent(v), r.noise[j]); };
   float best = -INFINITY, sum = 0.f;
   each_entry(x, a.vocab, [&](float v, int32_t j) {
     if (!cut.keeps(order_key(v), j)) return;
@@ -757,7 +759,7 @@ __device__ __forceinline__ Listed take_list(SampleShared& sh, int n, unsigned lo
   Best best;
   uint32_t hi = 0, lo = 0;
   const auto kept = [&](unsigned long long k) { return k >= cut && list_logit(k) >= min_x; };
-  const auto score = [&](float x, float e) { return e >= 0.f ? r.near_exponent(x) - __log2f(e) : -INFINITY; };
+  const auto score = [&](float x, float e) { return Row::score(r.near_exponent(x), e); };
   for (int i = tid; i < n; i += kThreads) {
     const unsigned long long k = sh.list[i];
     if (!kept(k)) continue;
