@@ -47,21 +47,26 @@ struct Teacher {
 constexpr int kNone = 0, kGood = 1, kNan = 2, kBad = 3;
 constexpr int kPerLane = DOBB_MAX_TEACHER / 32;
 
-// Ids seen so far, three bits each (a Bloom filter): 256 entries without a repeated id
-// are taken for some with one once in 16 rows, 64 entries once in 4000.
+// Ids of the rounds before, three bits each (a Bloom filter of multiplicative hashes: fields of
+// the product with 2^64 / golden ratio).  256 entries without a repeated id are taken for some with
+// one in one row of a hundred.
 constexpr int kSeenBits = 12;
 struct Seen {
   uint32_t word[3][(1 << kSeenBits) / 32];
-};
-__device__ __forceinline__ bool seen_before(Seen& s, int32_t id) {
-  bool all = true;
-#pragma unroll
-  for (int h = 0; h < 3; ++h) {
-    const uint32_t bit = (uint32_t)id * (h == 0 ? 0x9e3779b1u : h == 1 ? 0x85ebca77u : 0xc2b2ae3du) >> (32 - kSeenBits);
-    all &= (atomicOr(&s.word[h][bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1;
+  static __device__ __forceinline__ uint32_t bit(int32_t id, int h) {
+    return (uint32_t)((uint64_t)id * 0x9e3779b97f4a7c15ull >> (64 - (h + 1) * kSeenBits)) & ((1u << kSeenBits) - 1);
   }
-  return all;
-}
+  __device__ __forceinline__ bool has(int32_t id) const {
+    bool all = true;
+#pragma unroll
+    for (int h = 0; h < 3; ++h) all &= word[h][bit(id, h) >> 5] >> (bit(id, h) & 31) & 1;
+    return all;
+  }
+  __device__ __forceinline__ void add(int32_t id) {
+#pragma unroll
+    for (int h = 0; h < 3; ++h) atomicOr(&word[h][bit(id, h) >> 5], 1u << (bit(id, h) & 31));
+  }
+};
 
 // One warp reads the teacher's row: q and log q of every entry, and with SUMS the sum
 // of q over every id at its first entry.
@@ -82,7 +87,7 @@ __device__ __forceinline__ void load_teacher(Teacher& t, Seen* seen, const Disti
                             : static_cast<const float*>(a.teacher)[row * a.k + i];
     }
   }
-  if (SUMS) {
+  if (SUMS && a.k > 32) {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(Seen) / 16); i += 32) reinterpret_cast<uint4*>(seen)[i + lane] = make_uint4(0, 0, 0, 0);
     static_assert(sizeof(Seen) % 512 == 0, "cleared by a warp");
@@ -93,14 +98,25 @@ __device__ __forceinline__ void load_teacher(Teacher& t, Seen* seen, const Disti
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) {
     const int i = u * 32 + lane;
+    if (u * 32 >= a.k) break;
     if (ids[u] < 0) v[u] = -INFINITY;
     bad |= ids[u] >= a.vocab;
     any |= v[u] != -INFINITY;
     nan |= !(v[u] < INFINITY);
     own[u] = ids[u] < 0 || ids[u] >= a.vocab ? -1 : (int32_t)ids[u];
     if (i < a.k) t.id[i] = own[u];
-    if (SUMS && own[u] >= 0) twice |= seen_before(*seen, own[u]);
     m = fmaxf(m, v[u]);
+    if (SUMS) {
+      // the ids of one round against each other, then against those of the rounds before, which
+      // are all marked by then: no order of the lanes matters
+      const uint32_t equal = __match_any_sync(0xffffffffu, own[u]);
+      if (own[u] >= 0) twice |= (equal & (equal - 1)) != 0 || (u > 0 && seen->has(own[u]));
+      if ((u + 1) * 32 < a.k) {
+        __syncwarp();
+        if (own[u] >= 0) seen->add(own[u]);
+        __syncwarp();
+      }
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
