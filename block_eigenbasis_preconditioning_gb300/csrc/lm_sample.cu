@@ -98,6 +98,15 @@ struct Pair {
     lo += (hi - (t - z)) + (v - z);
     hi = t;
   }
+  __device__ __forceinline__ void add(const Pair& v) {
+    add(v.hi);
+    lo += v.lo;
+  }
+  __device__ __forceinline__ void scale(float f) {
+    hi *= f;
+    lo *= f;
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
 };
 
 // What a block of the cluster tells the first one: its candidate for the token.
@@ -127,7 +136,8 @@ struct SampleShared {
   unsigned long long few[kFew], few_mass[kFew];
   unsigned long long cut;
   Part part[kMaxParts];
-  float max[kMaxParts], ref[kMaxParts], sum[kMaxParts];
+  float max[kMaxParts], ref[kMaxParts];
+  float2 sum[kMaxParts];  // a pair
   float bound[kMaxParts][2];
   int32_t border[2];
   int32_t nlist, nfew;
@@ -199,18 +209,14 @@ __device__ __forceinline__ Pair block_pair_sum(Pair v, SampleShared& sh) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float h = __shfl_xor_sync(0xffffffffu, v.hi, o), l = __shfl_xor_sync(0xffffffffu, v.lo, o);
-    v.add(h);
-    v.lo += l;
+    v.add(Pair{h, l});
   }
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh.pairs[threadIdx.x >> 5] = make_float2(v.hi, v.lo);
   __syncthreads();
   Pair t;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    t.add(sh.pairs[w].x);
-    t.lo += sh.pairs[w].y;
-  }
+  for (int w = 0; w < kWarps; ++w) t.add(Pair{sh.pairs[w].x, sh.pairs[w].y});
   return t;
 }
 
@@ -1139,6 +1145,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
     float own = -INFINITY, ref = -kWide;
     bool nan = false;
     uint64_t s2 = 0, e2 = 0;
+    // top_p's total: a batch's sum goes to a pair at once, as a plain fp32 sum over a thread's
+    // entries would be off by up to their number times 2^-25 of itself (131072 nearly equal
+    // entries a row: 2^-19; half a million: 2^-17).  Costs 509 x 50257 bf16 with top_p 115 -> 116 us
+    Pair pair;
+    const auto flush = [&](float before) {  // the reference that the pair is relative to
+      if (ref != before) pair.scale(lm::exp2_fast(lm::max_nan(before - ref, -1000.f)));
+      float lo, hi;
+      lm::unpack2(s2, lo, hi);
+      pair.add(lo + hi);
+      s2 = 0;
+    };
     BestBatch best;
     float outside = single;  // this thread's entry outside the vectors or groups
     if (plain) {
@@ -1169,6 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
         }
         best.add(top, g0);
       }
+      flush(ref);
       outside = -INFINITY;
       if (gr.single >= 0) {
         outside = load_f32(x + gr.single);
@@ -1181,30 +1199,30 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
         uint4 v[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) v[u] = __ldg(sl.xv + v0 + u * sl.step);
+        const float before = ref;
         add_vectors<T, false>(v, r.c, c2, own, ref, s2, e2, nan);
+        if (top_p < 1.f) flush(before);
       }
+      const float before = ref;
 #pragma unroll 1
       for (; v0 < sl.nvec; v0 += sl.step) {
         const uint4 v[1] = {__ldg(sl.xv + v0)};
         add_vectors<T, false>(v, r.c, c2, own, ref, s2, e2, nan);
       }
+      flush(before);
     }
     // the block's maximum, reference and sum
     m = block_max(lm::max_nan(nan ? NAN : own, outside), sh.red, larger_nan);
-    float s, hi;
-    lm::unpack2(s2, s, hi);
-    s += hi;
     const float block_ref = reference(m, r.c);
-    float none = 0.f;
-    move_by(s, none, ref - block_ref);
-    s += lm::exp2_fast(lm::max_nan(fmaf(outside, r.c, -block_ref), -200.f));
-    s = block_sum(s, sh.red);
+    pair.scale(lm::exp2_fast(lm::max_nan(ref - block_ref, -1000.f)));
+    pair.add(lm::exp2_fast(lm::max_nan(fmaf(outside, r.c, -block_ref), -200.f)));
+    pair = block_pair_sum(pair, sh);
     all_started();
     if (tid < parts) {
       SampleShared* o = each(tid);
       o->max[rank] = m;
       o->ref[rank] = block_ref;
-      o->sum[rank] = s;
+      o->sum[rank] = make_float2(pair.hi, pair.lo);
     }
     // the block's candidate goes to the first block
     // (score: of a kept entry, -inf of others)
@@ -1270,9 +1288,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
     for (int p = 0; p < parts; ++p) m = lm::max_nan(m, sh.max[p]);
     if (ended(m)) return;
     const float row_ref = reference(m, r.c);
-    float total = 0.f;
-    for (int p = 0; p < parts; ++p) total += sh.sum[p] * lm::exp2_fast(fmaxf(sh.ref[p] - row_ref, -1000.f));
-    total *= lm::exp2_fast(-fmaf(m, r.c, -row_ref));  // relative to m c itself
+    // the row's sum relative to m c itself (asked for twice: two registers less in the last pass)
+    const auto total = [&] {
+      Pair t;
+      for (int p = 0; p < parts; ++p) {
+        Pair q{sh.sum[p].x, sh.sum[p].y};
+        q.scale(lm::exp2_fast(fmaxf(sh.ref[p] - row_ref, -1000.f)));
+        t.add(q);
+      }
+      t.scale(lm::exp2_fast(-fmaf(m, r.c, -row_ref)));
+      return t;
+    };
     r.m = m;
     general = !Row::near_zero(m, r.c);
     // the first block joins the candidates; false: the general way has to
@@ -1298,16 +1324,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
           if (at != was) q = o;
         }
       }
-      finish(q.at, kLn2 * (r.near_exponent(q.x) - log2f(fmaxf(kept.hi + kept.lo, 1.f))));
+      finish(q.at, kLn2 * (r.near_exponent(q.x) - log2f(fmaxf(kept.value(), 1.f))));
       return true;
     };
     if (plain) {
       if (rank != 0) return;
       Part none_listed;
       none_listed.at = -1;
-      Pair kept;
-      kept.add(total);
-      if (!general && decide(none_listed, kept)) return;
+      if (!general && decide(none_listed, total())) return;
       general = true;
     }
     if (!general) {
@@ -1322,7 +1346,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
         // spare, the lowest bin
         const float lowest = fmaxf(log2f((1.f - top_p) / (float)a.vocab) - 1.f, -60.f);
         const float per_bin = (float)(kBins - 1) / -lowest;  // bins per unit of log 2
-        const float total_ref = fmaf(m, r.c, log2f(total));
+        const float total_ref = fmaf(m, r.c, log2f(total().value()));
         const float low_x = fmaxf((total_ref + lowest) / r.c, -FLT_MAX);
         __syncthreads();
         const auto count = [&](float f) {
@@ -1445,10 +1469,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
       sync();
       if (rank != 0) return;
       Pair kept;
-      for (int p = 0; p < parts; ++p) {
-        kept.add(sh.part[p].mass.x);
-        kept.lo += sh.part[p].mass.y;
-      }
+      for (int p = 0; p < parts; ++p) kept.add(Pair{sh.part[p].mass.x, sh.part[p].mass.y});
       Part listed;
       listed.at = -1;
       general = false;
@@ -1456,11 +1477,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
         const int n = sh.nlist;
         // the border lies in the list, or the list goes to the row's end
         Pair rest;
-        const float share = top_p * total;
+        const Pair all = total();
+        const float share = top_p * all.hi;
         rest.add(share);
         rest.add(-kept.hi);
-        rest.add(fmaf(top_p, total, -share));
-        rest.add(-kept.lo);
+        rest.add(fmaf(top_p, all.hi, -share));
+        rest.add(fmaf(top_p, all.lo, -kept.lo));
         const unsigned long long want = whole_mass(rest);
         general = n > kList || want == 0;
         if (!general) {

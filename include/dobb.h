@@ -601,11 +601,11 @@ dobb_status dobb_distill_backward(const void* logits_dev, dobb_dtype logits_dtyp
  *   logp[r]   = y_token - log sum_{kept} e^y
  * For noise drawn independently from the exponential distribution with mean 1
  * token j comes out with probability e^{logp}.  The comparison is made in
- * 64 bits where fp32 might decide otherwise.  top_p's sums are good to about 2^-22
- * of the mass (an entry whose border is nearer falls on either side) and taken in a
- * fixed order or in whole numbers: the same call on the same data gives the same
- * tokens.  Noise is a positive number
- * for each logit; 0 wins over every other, NaN and negative numbers lose
+ * 64 bits where fp32 might decide otherwise.  top_p's sums are good to (3 W + 32) 2^-24
+ * of the mass, W the mean of |y - max y| over it (2^-18 for ordinary rows; an entry whose
+ * border is nearer falls on either side), and taken in a fixed order or in whole numbers: the
+ * same call on the same data gives the same tokens.  Noise is a positive
+ * number for each logit; 0 wins over every other, NaN and negative numbers lose
  * like +inf.  Noise of entries that are not kept is not looked at.
  *   scale   in (0, 2^127] (the inverse temperature); greedy choice is top_k 1
  *   scales, top_ks, top_ps, min_ps  rows values each, or NULL: then the one

@@ -2,6 +2,7 @@
 The bounds are those of test_gpu_lm_sample."""
 import numpy as np
 import pytest
+import torch
 
 from lm_util import dev, rounded
 from test_gpu_lm_sample import _check
@@ -42,3 +43,34 @@ def test_a_random_number_of_zero_wins_with_the_lowest_logit_too(xt):
             assert r.tokens.tolist() == [105] * 5 and bool((r.logp == -np.inf).all()), (vocab, scale, top_k)
             # among fewer the zero is not kept
             assert bool((d.sample(dev(x, xt), dev(e, "f32"), scale=scale, top_k=55).tokens < 50).all())
+
+
+def test_top_p_over_half_a_million_nearly_equal_masses():
+    """One block a row, three quarters of it one value whose sum rounds one way again and again (a plain
+    fp32 sum is off by up to 2^-17 of itself): what is kept is right to (3 W + 32) u of the mass, W the mean |log| of a
+    mass, u = 2^-24, as dobb.h has it.
+
+    Around the border the random numbers are tiny, the smaller the further behind: the token names the last entry kept."""
+    import block_eigenbasis_preconditioning_gb300 as d
+    rows, vocab, first, around = 312, 524288, 1024, 12
+    rng = np.random.default_rng(23)
+    behind = np.linspace(0.21, 0.9, 12)  # of the one value, in units of log 2
+    x = np.zeros((len(behind), vocab), dtype=np.float32)  # (the maximum first: nothing is moved later)
+    x[:, first:first + vocab * 3 // 4] = -np.log(2) * behind[:, None]
+    x[:, first + vocab * 3 // 4:] = rng.uniform(-3 * np.log(2), -np.log(2), size=(len(behind), vocab - first - vocab * 3 // 4))  # few near each border
+    order = np.argsort(-x, axis=1, kind="stable")
+    p = np.exp(np.take_along_axis(x, order, 1).astype(np.float64))
+    total, upto = p.sum(1), p.cumsum(1)
+    slack = (3 * (p * -np.log(p)).sum(1) / total + 32) * 2.0 ** -24 * total
+    which = np.arange(rows) % len(behind)
+    top_p = rng.uniform(0.92, 0.98, size=rows).astype(np.float32)
+    share = top_p.astype(np.float64) * total[which]
+    last = np.array([int(np.searchsorted(upto[r], s)) for r, s in zip(which, share)])  # before it lies less
+    noise = torch.ones(rows, vocab, device="cuda")
+    at = np.stack([order[r, n - around:n + around] for r, n in zip(which, last)])
+    noise.scatter_(1, torch.from_numpy(at).cuda(), torch.logspace(-3, -36, 2 * around, device="cuda").expand(rows, -1))
+    r = d.sample(torch.from_numpy(x).cuda()[torch.from_numpy(which).cuda()], noise, top_p=torch.from_numpy(top_p).cuda())
+    rank = np.argsort(order, axis=1)
+    kept = rank[which, r.tokens.cpu().numpy()]
+    off = np.maximum(upto[which, kept - 1] - share, share - upto[which, kept]) / slack[which]
+    assert (off <= 1).all(), f"{int((off > 1).sum())} of {rows} rows end {off.max():.1f} times too far from the border ({kept[off.argmax()] - last[off.argmax()]} entries)"
