@@ -1201,7 +1201,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
         for (int u = 0; u < kBatch; ++u) v[u] = __ldg(sl.xv + v0 + u * sl.step);
         const float before = ref;
         add_vectors<T, false>(v, r.c, c2, own, ref, s2, e2, nan);
-        if (top_p < 1.f) flush(before);
+        flush(before);
       }
       const float before = ref;
 #pragma unroll 1
