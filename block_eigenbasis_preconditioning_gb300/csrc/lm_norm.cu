@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward(const __grid_constan
       uint64_t w0, w1, b0, b1;
       read_four<float, P, ALIGNED>(w0, w1, weight, q, c);
       read_four<float, P, ALIGNED>(b0, b1, bias, q, c);
-      store_four<TO, P, ALIGNED>(out + row * a.out_stride, lm::fma2(lm::fma2(v[2 * q], h2, minus_m), lm::mul2(rstd, w0), b0),
-                                 lm::fma2(lm::fma2(v[2 * q + 1], h2, minus_m), lm::mul2(rstd, w1), b1), q, c);
+      // (rstd times the weight first could leave fp32 where the result does not)
+      store_four<TO, P, ALIGNED>(out + row * a.out_stride, lm::fma2(lm::mul2(lm::fma2(v[2 * q], h2, minus_m), rstd), w0, b0),
+                                 lm::fma2(lm::mul2(lm::fma2(v[2 * q + 1], h2, minus_m), rstd), w1, b1), q, c);
     }
   }
 }
