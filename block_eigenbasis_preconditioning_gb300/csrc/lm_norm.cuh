@@ -11,6 +11,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "lm_common.cuh"
@@ -240,6 +241,9 @@ __device__ __forceinline__ float param(const void* p, int bf16, int64_t i) {
 // xh of an entry is (x h - mean) rstd: h = 1, or 2^-100 in rows whose sums or
 // differences would leave fp32.
 constexpr float kDown = 0x1p-100f;
+// rstd of a row scaled down.  Beyond fp32 (rstd above 2^28 although entries of 2^100 have
+// neighbours 2^77 away) only where every difference is 0: any finite factor will do.
+__device__ __forceinline__ float in_range(float scaled) { return scaled == INFINITY ? FLT_MAX : scaled; }
 struct RowScale {
   float h, mean, rstd;
   __device__ __forceinline__ float xhat(float x) const { return fmaf(x, h, -mean) * rstd; }
@@ -255,13 +259,13 @@ __device__ __forceinline__ RowScale row_scale(float h, float mean, float var, fl
   const double rstd = 1.0 / sqrt((double)var * 0x1p200 + (double)eps);
   row_mean = mean * 0x1p100f;
   row_rstd = (float)rstd;
-  return {h, mean, (float)(rstd * 0x1p100)};
+  return {h, mean, in_range((float)(rstd * 0x1p100))};
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 __device__ __forceinline__ RowScale given_scale(float mean, float rstd) {
   const float h = fabsf(mean) < 0x1p100f && rstd > kDown ? 1.f : kDown;
-  return {h, mean * h, h == 1.f ? rstd : rstd * 0x1p100f};
+  return {h, mean * h, h == 1.f ? rstd : in_range(rstd * 0x1p100f)};
 }
 
 // A block's sum of f(i), i < n: eight at a time of each thread in fp32, then in fp64.
