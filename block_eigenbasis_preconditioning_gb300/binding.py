@@ -108,6 +108,9 @@ SIGNATURES = [
                                                    _c.c_int64, _c.c_int, _I64P]),
     ("dobb_distill", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int, _VP, _c.c_int,
                                 _c.c_int, _c.c_float, _c.c_float, _VP, _VP, _VP, _VP, _VP, _c.c_int64, _VP, _VP]),
+    ("dobb_selftest_distill_timeout", _c.c_int,
+     [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int, _VP, _c.c_int, _c.c_int, _c.c_float, _c.c_float, _VP, _VP, _VP, _VP,
+      _VP, _c.c_int64, _VP, _VP, _c.c_int64, _c.c_int, _c.c_uint64]),
     ("dobb_distill_backward", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int, _VP,
                                          _c.c_int, _c.c_int, _c.c_float, _c.c_float, _VP, _VP, _VP, _VP,
                                          _c.c_int64, _VP]),

@@ -332,6 +332,14 @@ constexpr int kMaxParts = 8;
 constexpr int kSms = 152;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// How long a wait lasts at most, and (self-test) the block of a cluster that copies in no row
+// from `loaded` on.
+struct Patience {
+  uint64_t limit = kWaitNs;
+  int64_t loaded = 0;
+  int32_t late_part = -1;
+};
+
 struct RowTeacher {
   Teacher t;
   float x[DOBB_MAX_TEACHER];  // the logits of its entries
@@ -340,8 +348,8 @@ struct RowShared {
   uint64_t full[kMaxStages], empty[kMaxStages], ready, written, parts_in[2];
   __align__(16) Seen seen;
   RowTeacher teacher[2];
-  float2 part[2][kMaxParts];  // maximum and sum of every block's stretch
-  float2 stat[2];             // row_max and log_sum
+  float2 part[2][kMaxParts];  // maximum and sum of every block's stretch; a maximum of NaN: it gave up
+  float2 stat[2];             // row_max and log_sum, NaN where a block gave up
   float red[2][kComputeWarps];
   int32_t late;               // a wait gave up: all others do
 };
@@ -403,7 +411,7 @@ struct Stretch {  // of one row
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs a, int32_t per, uint64_t limit) {
+__global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs a, int32_t per, const Patience patience) {
   using V = lm::Vec16<T>;
   extern __shared__ __align__(128) unsigned char raw[];
   RowShared& sh = *reinterpret_cast<RowShared*>(raw);
@@ -429,6 +437,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
   __syncthreads();
   if (parts > 1) cluster.sync();
   const float c = a.scale * kLog2e;
+  const uint64_t limit = patience.limit;
 
   if (warp == kComputeWarps) {
     // ---- producer
@@ -438,6 +447,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
     for (int s = 0; s < kMaxStages; ++s) issued[s] = 0;
     bool ok = true;
     for (int64_t row = first; row < a.rows && ok; row += step) {
+      if (rank == patience.late_part && row >= patience.loaded) break;
       const Stretch<T> r(a, row, lo, n);
 #pragma unroll
       for (int s = 0; s < kMaxStages; ++s) {
@@ -481,13 +491,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
       const bool ok = row_wait(sh, &sh.written, it & 1, limit);
       __syncwarp();
       const float2 st = sh.stat[it & 1];
-      const bool lost = !ok || *(volatile int32_t*)&sh.late;
+      // a wait of this block gave up, or one of another block of the cluster
+      const bool lost = !ok || *(volatile int32_t*)&sh.late || !(st.x == st.x);
+      if (lost && lane == 0 && a.flags) atomicOr(a.flags, DOBB_FLAG_TIMEOUT);
       if (rank == 0) {
-        write_loss(a, q.t, row, lost ? NAN : st.x, lost ? NAN : st.y, [&](int i) { return q.x[i]; });
+        if (!lost) write_loss(a, q.t, row, st.x, st.y, [&](int i) { return q.x[i]; });
         if (lane == 0) {
+          if (lost) a.loss[row] = NAN;
           a.row_max[row] = lost ? NAN : st.x;
           a.log_sum[row] = lost ? NAN : st.y;
-          if (lost && a.flags) atomicOr(a.flags, DOBB_FLAG_TIMEOUT);
         }
       }
       const Dense dense(st.x, st.y, a.scale, a.g[row], q.t.state);
@@ -572,10 +584,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
     s = 0.f;
 #pragma unroll
     for (int w = 0; w < kComputeWarps; ++w) s += sh.red[1][w];
-    if (*(volatile int32_t*)&sh.late) s = NAN;
     if (parts > 1) {
       const int buf = it & 1;
-      if (tid < parts) send_part(&sh.part[buf][rank], &sh.parts_in[buf], tid, m, s);
+      if (tid < parts) send_part(&sh.part[buf][rank], &sh.parts_in[buf], tid, *(volatile int32_t*)&sh.late ? NAN : m, s);
       const uint64_t t0 = ptx::global_timer_ns();
       while (!try_wait_cluster(&sh.parts_in[buf], (it >> 1) & 1)) {
         if (ptx::global_timer_ns() - t0 > limit) {
@@ -584,7 +595,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
           break;
         }
       }
-      for (int p = 0; p < parts; ++p) m = fmaxf(m, sh.part[buf][p].x);
+      for (int p = 0; p < parts; ++p) {
+        m = fmaxf(m, sh.part[buf][p].x);
+        ok = ok && sh.part[buf][p].x == sh.part[buf][p].x;
+      }
       s = 0.f;
       for (int p = 0; p < parts; ++p) {
         const float2 q = sh.part[buf][p];
@@ -594,11 +608,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) distill_rows(const DistillArgs
       }
     }
     float log_sum = kLn2 * log2f(s);
-    if (!ok || *(volatile int32_t*)&sh.late) log_sum = NAN;
+    if (!ok || *(volatile int32_t*)&sh.late) m = log_sum = NAN;
     if (tid == 0) sh.stat[it & 1] = make_float2(m, log_sum);
 
     // ---- the gradient, in vectors on the output's boundaries
-    const Dense dense(m, log_sum, a.scale, a.g[row], sh.teacher[it & 1].t.state);
+    // (in a row that is given up the teacher may be another row's)
+    const Dense dense(m, log_sum, a.scale, a.g[row], m == m ? sh.teacher[it & 1].t.state : kNan);
     const int32_t dhead = (int32_t)lm::head_of(r.d, n), dvec = (n - dhead) / V::N, dtail0 = dhead + dvec * V::N;
     const uint32_t shift = (uint32_t)((dhead - r.head) * (int32_t)sizeof(T)) & 15;
     uint4* dv = reinterpret_cast<uint4*>(r.d + dhead);
@@ -725,7 +740,7 @@ int row_parts(int64_t rows, int64_t vocab, size_t bytes) {
 }
 
 template <typename T>
-cudaError_t launch_rows(DistillArgs a, int parts, cudaStream_t s) {
+cudaError_t launch_rows(const DistillArgs& a, int parts, const Patience& patience, cudaStream_t s) {
   // stretches of whole 16-byte vectors
   const int32_t per = (int32_t)(((a.vocab + parts - 1) / parts + 7) / 8 * 8);
   const size_t smem = (sizeof(RowShared) + 127) / 128 * 128 + 16 + (size_t)per * sizeof(T) + 32;
@@ -748,16 +763,15 @@ cudaError_t launch_rows(DistillArgs a, int parts, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   cfg.gridDim = dim3((unsigned)(std::min<int64_t>(a.rows, std::max(clusters, 1)) * parts));
-  return cudaLaunchKernelEx(&cfg, distill_rows<T>, a, per, kWaitNs);
+  return cudaLaunchKernelEx(&cfg, distill_rows<T>, a, per, patience);
 }
 
-}  // namespace
-
-extern "C" dobb_status dobb_distill(const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab,
+// selftest: with the waits' limit and the withheld rows of `patience`, and no other way than the clusters'
+dobb_status distill(const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab,
                                     int64_t row_stride, const void* ids, int id_bytes, const void* teacher,
                                     dobb_dtype teacher_dtype, int k, float scale, float teacher_scale, float* loss,
                                     float* row_max, float* log_sum, const float* grad_loss, void* dlogits,
-                                    int64_t out_stride, uint32_t* flags, void* stream) {
+                                    int64_t out_stride, uint32_t* flags, void* stream, Patience patience, bool selftest) {
   dobb_status st = check_distill(logits, logits_dtype, rows, vocab, row_stride, ids, id_bytes, teacher, teacher_dtype, k, scale,
                                  teacher_scale, grad_loss || dlogits, grad_loss, dlogits, out_stride);
   if (st != DOBB_OK || rows == 0) return st;
@@ -776,8 +790,11 @@ extern "C" dobb_status dobb_distill(const void* logits, dobb_dtype logits_dtype,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f32 = logits_dtype == DOBB_F32;
   const int parts = dlogits ? row_parts(rows, vocab, lm::dtype_bytes(logits_dtype)) : 0;
+  if (selftest && (parts == 0 || patience.late_part < 0 || patience.late_part >= parts))
+    return parts ? fail(DOBB_ERR_INVALID_ARG, "late_part must lie in [0, %d) (got %d)", parts, patience.late_part)
+                 : fail(DOBB_ERR_UNSUPPORTED, "this call waits for no copies");
   if (parts) {
-    const cudaError_t e = f32 ? launch_rows<float>(a, parts, s) : launch_rows<__nv_bfloat16>(a, parts, s);
+    const cudaError_t e = f32 ? launch_rows<float>(a, parts, patience, s) : launch_rows<__nv_bfloat16>(a, parts, patience, s);
     if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "distillation launch: %s", cudaGetErrorString(e));
     return DOBB_OK;
   }
@@ -792,6 +809,29 @@ extern "C" dobb_status dobb_distill(const void* logits, dobb_dtype logits_dtype,
   if (e == cudaSuccess && dlogits) e = f32 ? launch_backward<float>(a, s) : launch_backward<__nv_bfloat16>(a, s);
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "distillation launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
+}
+
+}  // namespace
+
+extern "C" dobb_status dobb_distill(const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab,
+                                    int64_t row_stride, const void* ids, int id_bytes, const void* teacher,
+                                    dobb_dtype teacher_dtype, int k, float scale, float teacher_scale, float* loss,
+                                    float* row_max, float* log_sum, const float* grad_loss, void* dlogits,
+                                    int64_t out_stride, uint32_t* flags, void* stream) {
+  return distill(logits, logits_dtype, rows, vocab, row_stride, ids, id_bytes, teacher, teacher_dtype, k, scale, teacher_scale, loss,
+                 row_max, log_sum, grad_loss, dlogits, out_stride, flags, stream, Patience{}, false);
+}
+
+extern "C" dobb_status dobb_selftest_distill_timeout(const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab,
+                                                     int64_t row_stride, const void* ids, int id_bytes, const void* teacher,
+                                                     dobb_dtype teacher_dtype, int k, float scale, float teacher_scale, float* loss,
+                                                     float* row_max, float* log_sum, const float* grad_loss, void* dlogits,
+                                                     int64_t out_stride, uint32_t* flags, void* stream, int64_t loaded_rows,
+                                                     int late_part, uint64_t timeout_ns) {
+  if (loaded_rows < 0 || loaded_rows > rows || timeout_ns == 0 || timeout_ns > 5000000000ull)
+    return fail(DOBB_ERR_INVALID_ARG, "loaded_rows must lie in [0, rows], timeout_ns in [1, 5e9]");
+  return distill(logits, logits_dtype, rows, vocab, row_stride, ids, id_bytes, teacher, teacher_dtype, k, scale, teacher_scale, loss,
+                 row_max, log_sum, grad_loss, dlogits, out_stride, flags, stream, Patience{timeout_ns, loaded_rows, late_part}, true);
 }
 
 extern "C" dobb_status dobb_distill_backward(const void* logits, dobb_dtype logits_dtype, int64_t rows, int64_t vocab,

@@ -578,6 +578,21 @@ dobb_status dobb_distill(const void* logits_dev, dobb_dtype logits_dtype, int64_
                          float* log_sum_dev, const float* grad_loss_dev, void* dlogits_dev,
                          int64_t out_stride, uint32_t* flags_dev, void* stream);
 
+/* Self-test of those bounded waits: dobb_distill with the gradient, a limit of
+ * timeout_ns (1 ns ... 5 s), and in every group of blocks that share a row the block
+ * late_part (0 for the first) copying in only the first loaded_rows rows, so that the waits
+ * for the others run out.  DOBB_ERR_UNSUPPORTED for sizes that are computed without
+ * such waits, DOBB_ERR_INVALID_ARG where there is no such block. */
+dobb_status dobb_selftest_distill_timeout(const void* logits_dev, dobb_dtype logits_dtype,
+                                          int64_t rows, int64_t vocab, int64_t row_stride,
+                                          const void* ids_dev, int id_bytes, const void* teacher_dev,
+                                          dobb_dtype teacher_dtype, int k, float scale,
+                                          float teacher_scale, float* loss_dev, float* row_max_dev,
+                                          float* log_sum_dev, const float* grad_loss_dev,
+                                          void* dlogits_dev, int64_t out_stride,
+                                          uint32_t* flags_dev, void* stream, int64_t loaded_rows,
+                                          int late_part, uint64_t timeout_ns);
+
 /* The gradient alone, given the row_max and log_sum of a dobb_distill call (or
  * of dobb_log_probs with the same scale) on the same logits. */
 dobb_status dobb_distill_backward(const void* logits_dev, dobb_dtype logits_dtype, int64_t rows,
