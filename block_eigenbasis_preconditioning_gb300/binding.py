@@ -104,6 +104,12 @@ SIGNATURES = [
     ("dobb_layer_norm_backward", _c.c_int, [_VP, _c.c_int, _c.c_int64, _VP, _c.c_int, _c.c_int64, _c.c_int64,
                                             _c.c_int64, _VP, _c.c_int, _VP, _VP, _VP, _c.c_int64, _VP, _VP,
                                             _c.c_int, _c.c_int, _VP, _c.c_size_t, _VP]),
+    ("dobb_selftest_layer_norm_timeout", _c.c_int,
+     [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _VP, _c.c_int, _c.c_float, _VP, _c.c_int, _c.c_int64, _VP, _VP, _VP,
+      _c.c_int64, _c.c_uint64]),
+    ("dobb_selftest_layer_norm_backward_timeout", _c.c_int,
+     [_VP, _c.c_int, _c.c_int64, _VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int, _VP, _VP, _VP, _c.c_int64, _VP, _VP,
+      _c.c_int, _c.c_int, _VP, _c.c_size_t, _VP, _c.c_int64, _c.c_uint64]),
     ("dobb_selftest_layer_norm_smem", _c.c_int64, [_c.c_int64, _c.c_int64, _c.c_int, _c.c_int64, _c.c_int,
                                                    _c.c_int64, _c.c_int, _I64P]),
     ("dobb_distill", _c.c_int, [_VP, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _VP, _c.c_int, _VP, _c.c_int,

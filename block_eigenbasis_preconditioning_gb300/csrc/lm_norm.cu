@@ -16,20 +16,21 @@ struct NormArgs {
   float *mean, *rstd;
   Shape shape;
   Ring ring;
+  Patience patience;
 };
 
 // The forward pass's: a lane for each group.
 template <typename TX>
 __device__ __forceinline__ void produce_groups(GroupBarriers& b, unsigned char* raw, const Ring& ring, const Shape& shape, const TX* x,
-                                               int64_t stride, int64_t rows, int32_t dim) {
+                                               int64_t stride, int64_t rows, int32_t dim, const Patience& patience) {
   const int group = threadIdx.x & 31, unit = 32 / shape.lanes;
   if (group >= shape.groups) return;
   const TX* end = x + (rows - 1) * stride + dim;
   uint32_t k = 0;
   bool ok = true;
-  for (int64_t r0 = (int64_t)blockIdx.x * ring.rows + group * unit; r0 < rows && ok; r0 += (int64_t)gridDim.x * ring.rows, ++k) {
+  for (int64_t r0 = (int64_t)blockIdx.x * ring.rows + group * unit; r0 < patience.loaded && ok; r0 += (int64_t)gridDim.x * ring.rows, ++k) {
     const uint32_t s = group * ring.slots + k % ring.slots, turn = k / ring.slots;
-    if (turn > 0 && !(ok = ring_wait(b, &b.empty[s], (turn - 1) & 1))) break;
+    if (turn > 0 && !(ok = ring_wait(b, &b.empty[s], (turn - 1) & 1, patience.limit))) break;
     const int32_t count = (int32_t)min((int64_t)unit, rows - r0);
     unsigned char* to = raw + (size_t)s * ring.slot_bytes;
     uint32_t bytes = 0;
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward(const __grid_constan
   const int warp = threadIdx.x >> 5;
   ring_init(bar, sp.groups * a.ring.slots, sp.warps);
   if (warp == warps) {
-    produce_groups<TX>(bar, ring, a.ring, sp, x, a.x_stride, a.rows, a.dim);
+    produce_groups<TX>(bar, ring, a.ring, sp, x, a.x_stride, a.rows, a.dim, a.patience);
     return;
   }
   copy_params(weight, a.weight, a.param_bf16, a.dim, 1.f, warps * 32);
@@ -76,9 +77,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward(const __grid_constan
   int buf = 0;
   const int unit = 32 / sp.lanes, mine = in_warp / sp.lanes;  // rows of the group at a time, this lane's of them
   uint32_t slot = 0, phase = 0;
+  bool ok = true;  // once a wait gave up the phases are not known any more: all later rows are lost
   for (int64_t row0 = (int64_t)blockIdx.x * a.ring.rows + group * unit; row0 < a.rows; row0 += (int64_t)gridDim.x * a.ring.rows) {
     const uint32_t s = group * a.ring.slots + slot;
-    const bool ok = __all_sync(0xffffffffu, ring_wait(bar, &bar.full[s], phase));
+    ok = __all_sync(0xffffffffu, ok && ring_wait(bar, &bar.full[s], phase, a.patience.limit));
     if (++slot == (uint32_t)a.ring.slots) {
       slot = 0;
       phase ^= 1;
@@ -121,7 +123,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward(const __grid_constan
       mean = m;
       var = m2;
       if (sp.warps > 1) {
-        if (in_warp == 0) red[buf][warp] = make_float2(m, m2);
+        // (a warp whose wait gave up: the whole row is lost)
+        if (in_warp == 0) red[buf][warp] = ok ? make_float2(m, m2) : make_float2(NAN, NAN);
         __syncwarp();
         group_sync(group, sp.warps * 32);
         mean = 0.f;
@@ -209,14 +212,10 @@ cudaError_t launch_forward(const NormArgs& a, const Plan& p, bool aligned, cudaS
                     : go(std::integral_constant<int, 8>{});
 }
 
-}  // namespace
-}  // namespace dobb
-
-using namespace dobb;
-
-extern "C" dobb_status dobb_layer_norm(const void* x, dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
-                                       const void* weight, const void* bias, dobb_dtype param_dtype, float eps, void* out,
-                                       dobb_dtype out_dtype, int64_t out_stride, float* mean, float* rstd, void* stream) {
+// selftest: the waits' limit and the rows that are copied in, or NULL
+dobb_status layer_norm(const void* x, dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride, const void* weight,
+                       const void* bias, dobb_dtype param_dtype, float eps, void* out, dobb_dtype out_dtype, int64_t out_stride,
+                       float* mean, float* rstd, void* stream, const Patience* selftest) {
   dobb_status st = check_norm(rows, dim, x_dtype, x_stride, out_dtype, out_stride, param_dtype);
   if (st != DOBB_OK) return st;
   if (!(eps >= 0x1p-126f && eps < INFINITY))
@@ -237,9 +236,10 @@ extern "C" dobb_status dobb_layer_norm(const void* x, dobb_dtype x_dtype, int64_
   ext.write("rstd", rstd, 1, rows, rows, DOBB_F32);
   if ((st = ext.check()) != DOBB_OK) return st;
   Plan p = plan(rows, dim, false);
+  if (selftest && p.wide) return fail(DOBB_ERR_UNSUPPORTED, "this call waits for no copies");
   const Ring ring = p.wide ? Ring{} : forward_ring(p, rows, dim, x_stride, x_dtype);
   const NormArgs a{x,   rows,       x_stride, (int32_t)dim, weight, bias, param_dtype == DOBB_BF16, eps,
-                   out, out_stride, mean,     rstd,         p.shape, ring};
+                   out, out_stride, mean,     rstd,         p.shape, ring,   selftest ? *selftest : Patience{kWaitNs, rows}};
   const bool aligned = dim % 4 == 0 && aligned_rows(x, x_stride, x_dtype, rows) && aligned_rows(out, out_stride, out_dtype, rows);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
@@ -248,6 +248,27 @@ extern "C" dobb_status dobb_layer_norm(const void* x, dobb_dtype x_dtype, int64_
                       : (out_dtype == DOBB_F32 ? launch_forward<bf16, float>(a, p, aligned, s) : launch_forward<bf16, bf16>(a, p, aligned, s));
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "layer norm launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
+}
+
+}  // namespace
+}  // namespace dobb
+
+using namespace dobb;
+
+extern "C" dobb_status dobb_layer_norm(const void* x, dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                                       const void* weight, const void* bias, dobb_dtype param_dtype, float eps, void* out,
+                                       dobb_dtype out_dtype, int64_t out_stride, float* mean, float* rstd, void* stream) {
+  return layer_norm(x, x_dtype, rows, dim, x_stride, weight, bias, param_dtype, eps, out, out_dtype, out_stride, mean, rstd, stream, nullptr);
+}
+
+extern "C" dobb_status dobb_selftest_layer_norm_timeout(const void* x, dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                                                        const void* weight, const void* bias, dobb_dtype param_dtype, float eps,
+                                                        void* out, dobb_dtype out_dtype, int64_t out_stride, float* mean, float* rstd,
+                                                        void* stream, int64_t loaded_rows, uint64_t timeout_ns) {
+  const Patience patience{timeout_ns, loaded_rows};
+  if (const dobb_status st = check_patience(patience, rows); st != DOBB_OK) return st;
+  return layer_norm(x, x_dtype, rows, dim, x_stride, weight, bias, param_dtype, eps, out, out_dtype, out_stride, mean, rstd, stream,
+                    &patience);
 }
 
 extern "C" int64_t dobb_selftest_layer_norm_smem(int64_t rows, int64_t dim, dobb_dtype x_dtype, int64_t x_stride, dobb_dtype grad_dtype,

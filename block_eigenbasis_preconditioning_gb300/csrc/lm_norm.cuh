@@ -168,6 +168,12 @@ struct GroupBarriers {
   int32_t late;
 };
 constexpr uint64_t kWaitNs = 2000000000ull;
+// How long a wait lasts at most, and how many rows are copied in (all of them but in the
+// self-test of the waits).
+struct Patience {
+  uint64_t limit;
+  int64_t loaded;
+};
 
 template <typename B>
 __device__ __forceinline__ void ring_init(B& b, int slots, int arrivals) {
@@ -182,12 +188,12 @@ __device__ __forceinline__ void ring_init(B& b, int slots, int arrivals) {
   __syncthreads();
 }
 template <typename B>
-__device__ __forceinline__ bool ring_wait(B& b, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool ring_wait(B& b, uint64_t* bar, uint32_t parity, uint64_t limit) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::global_timer_ns();
   while (!ptx::mbar_try_wait(bar, parity)) {
     if (*(volatile int32_t*)&b.late) return false;
-    if (ptx::global_timer_ns() - t0 > kWaitNs) {
+    if (ptx::global_timer_ns() - t0 > limit) {
       *(volatile int32_t*)&b.late = 1;
       return false;
     }
@@ -379,6 +385,12 @@ dobb_status check_norm(int64_t rows, int64_t dim, int x_dtype, int64_t x_stride,
     return fail(DOBB_ERR_INVALID_ARG, "a row stride is below dim %lld", (long long)dim);
   if (rows > 1 && (x_stride > INT64_MAX / 8 / rows || other_stride > INT64_MAX / 8 / rows))
     return fail(DOBB_ERR_UNSUPPORTED, "rows times a row stride is too large");
+  return DOBB_OK;
+}
+
+dobb_status check_patience(const Patience& p, int64_t rows) {
+  if (p.loaded < 0 || p.loaded > rows || p.limit == 0 || p.limit > 5000000000ull)
+    return fail(DOBB_ERR_INVALID_ARG, "loaded_rows must lie in [0, rows], timeout_ns in [1, 5e9]");
   return DOBB_OK;
 }
 

@@ -18,6 +18,7 @@ struct NormGradArgs {
   int32_t row_blocks;
   Shape shape;
   Ring ring;
+  Patience patience;
 };
 
 struct JoinArgs {
@@ -35,15 +36,15 @@ __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.lau
 // threads takes.
 template <typename TX, typename TG>
 __device__ __forceinline__ void produce(RingBarriers& b, unsigned char* raw, const Ring& ring, const TX* x, int64_t x_stride, const TG* g,
-                                        int64_t g_stride, int64_t rows, int32_t dim) {
+                                        int64_t g_stride, int64_t rows, int32_t dim, const Patience& patience) {
   const int lane = threadIdx.x & 31;
   const TX* x_end = x + (rows - 1) * x_stride + dim;
   const TG* g_end = g + (rows - 1) * g_stride + dim;
   uint32_t k = 0;
   bool ok = true;
-  for (int64_t r0 = (int64_t)blockIdx.x * ring.rows; r0 < rows && ok; r0 += (int64_t)gridDim.x * ring.rows, ++k) {
+  for (int64_t r0 = (int64_t)blockIdx.x * ring.rows; r0 < patience.loaded && ok; r0 += (int64_t)gridDim.x * ring.rows, ++k) {
     const uint32_t slot = k % ring.slots, turn = k / ring.slots;
-    if (turn > 0) ok = __all_sync(0xffffffffu, ring_wait(b, &b.empty[slot], (turn - 1) & 1));
+    if (turn > 0) ok = __all_sync(0xffffffffu, ring_wait(b, &b.empty[slot], (turn - 1) & 1, patience.limit));
     if (!ok) break;
     const int32_t count = (int32_t)min((int64_t)ring.rows, rows - r0);
     unsigned char* to = raw + (size_t)slot * ring.slot_bytes;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const __grid_consta
 #pragma unroll
   for (int i = 0; i < 4 * P; ++i) dw[i] = db[i] = 0;
   if (warp == warps) {
-    produce<TX, TG>(bar, ring, a.ring, x, a.x_stride, g, a.grad_stride, a.rows, a.dim);
+    produce<TX, TG>(bar, ring, a.ring, x, a.x_stride, g, a.grad_stride, a.rows, a.dim, a.patience);
   } else {
     copy_params(weight, a.weight, a.param_bf16, a.dim, 1.f, warps * 32);
     TX* dx = static_cast<TX*>(a.dx);
@@ -117,8 +118,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const __grid_consta
     asm volatile("bar.sync 15, %0;" ::"r"(warps * 32) : "memory");  // the parameters are there
     int buf = 0;
     uint32_t slot = 0, phase = 0;
+    bool ok = true;  // once a wait gave up the phases are not known any more: all later rows are lost
     for (; row - mine < a.rows; row += step) {
-      const bool ok = __all_sync(0xffffffffu, ring_wait(bar, &bar.full[slot], phase));
+      ok = __all_sync(0xffffffffu, ok && ring_wait(bar, &bar.full[slot], phase, a.patience.limit));
       uint64_t xh[4 * P], gv[4 * P];
       const RowScale r = given_scale(next_mean, next_rstd);
       const float rstd = ok ? next_rstd : NAN;
@@ -163,7 +165,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const __grid_consta
             t2 = lm::fma2(gi, xi, t2);
           }
         }
-        if (!ok) db[0] = both(NAN);
+        if (!ok) {
+#pragma unroll
+          for (int i = 0; i < 4 * P; ++i) db[i] = both(NAN);
+        }
       }
       float s1 = sum2(t1), s2 = sum2(t2);
       if (sp.lanes == 32) {
@@ -349,12 +354,14 @@ extern "C" size_t dobb_layer_norm_backward_bytes(int64_t rows, int64_t dim) {
   return workspace_bytes_of(plan(std::max<int64_t>(rows, 1), dim, true), rows, dim);
 }
 
-extern "C" dobb_status dobb_layer_norm_backward(const void* grad, dobb_dtype grad_dtype, int64_t grad_stride, const void* x,
-                                                dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
-                                                const void* weight, dobb_dtype param_dtype, const float* mean,
-                                                const float* rstd, void* dx, int64_t dx_stride, void* dweight, void* dbias,
-                                                dobb_dtype dparam_dtype, int accumulate, void* workspace,
-                                                size_t workspace_bytes, void* stream) {
+namespace {
+
+// selftest: the waits' limit and the rows that are copied in, or NULL
+dobb_status layer_norm_backward(const void* grad, dobb_dtype grad_dtype, int64_t grad_stride, const void* x, dobb_dtype x_dtype,
+                                int64_t rows, int64_t dim, int64_t x_stride, const void* weight, dobb_dtype param_dtype,
+                                const float* mean, const float* rstd, void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                dobb_dtype dparam_dtype, int accumulate, void* workspace, size_t workspace_bytes, void* stream,
+                                const Patience* selftest) {
   dobb_status st = check_norm(rows, dim, x_dtype, x_stride, grad_dtype, grad_stride, param_dtype);
   if (st != DOBB_OK) return st;
   if (lm::bad_dtype(dparam_dtype)) return fail(DOBB_ERR_INVALID_ARG, "every dtype must be DOBB_F32 or DOBB_BF16");
@@ -391,12 +398,14 @@ extern "C" dobb_status dobb_layer_norm_backward(const void* grad, dobb_dtype gra
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool params = dweight || dbias;
   Plan p = plan(std::max<int64_t>(rows, 1), dim, true);
+  if (selftest && p.wide) return fail(DOBB_ERR_UNSUPPORTED, "this call waits for no copies");
   float* partial = static_cast<float*>(workspace);
   cudaError_t e = cudaSuccess;
   if (rows > 0) {
     NormGradArgs a{grad,   x,      rows, grad_stride, x_stride, (int32_t)dim, weight, param_dtype == DOBB_BF16, mean, rstd, dx, dx_stride,
                    params ? partial : nullptr,
-                   reinterpret_cast<float2*>(static_cast<char*>(workspace) + partial_bytes(p, dim)), p.partials, p.shape, {}};
+                   reinterpret_cast<float2*>(static_cast<char*>(workspace) + partial_bytes(p, dim)), p.partials, p.shape, {},
+                   selftest ? *selftest : Patience{kWaitNs, rows}};
     if (!p.wide) a.ring = ring_of(p, rows, dim, x_stride, x_dtype, grad_stride, grad_dtype, true);
     const bool aligned = dim % 4 == 0 && aligned_rows(x, x_stride, x_dtype, rows) && aligned_rows(grad, grad_stride, grad_dtype, rows) &&
                          (!dx || aligned_rows(dx, dx_stride, x_dtype, rows));
@@ -413,4 +422,27 @@ extern "C" dobb_status dobb_layer_norm_backward(const void* grad, dobb_dtype gra
   }
   if (e != cudaSuccess) return fail(DOBB_ERR_CUDA, "layer norm gradient launch: %s", cudaGetErrorString(e));
   return DOBB_OK;
+}
+
+}  // namespace
+
+extern "C" dobb_status dobb_layer_norm_backward(const void* grad, dobb_dtype grad_dtype, int64_t grad_stride, const void* x,
+                                                dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride,
+                                                const void* weight, dobb_dtype param_dtype, const float* mean,
+                                                const float* rstd, void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                                dobb_dtype dparam_dtype, int accumulate, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  return layer_norm_backward(grad, grad_dtype, grad_stride, x, x_dtype, rows, dim, x_stride, weight, param_dtype, mean, rstd, dx, dx_stride, dweight, dbias,
+                             dparam_dtype, accumulate, workspace, workspace_bytes, stream, nullptr);
+}
+
+extern "C" dobb_status dobb_selftest_layer_norm_backward_timeout(
+    const void* grad, dobb_dtype grad_dtype, int64_t grad_stride, const void* x, dobb_dtype x_dtype, int64_t rows, int64_t dim,
+    int64_t x_stride, const void* weight, dobb_dtype param_dtype, const float* mean, const float* rstd, void* dx, int64_t dx_stride,
+    void* dweight, void* dbias, dobb_dtype dparam_dtype, int accumulate, void* workspace, size_t workspace_bytes, void* stream,
+    int64_t loaded_rows, uint64_t timeout_ns) {
+  const Patience patience{timeout_ns, loaded_rows};
+  if (const dobb_status st = check_patience(patience, rows); st != DOBB_OK) return st;
+  return layer_norm_backward(grad, grad_dtype, grad_stride, x, x_dtype, rows, dim, x_stride, weight, param_dtype, mean, rstd, dx, dx_stride, dweight, dbias,
+                             dparam_dtype, accumulate, workspace, workspace_bytes, stream, &patience);
 }

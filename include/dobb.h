@@ -502,7 +502,9 @@ dobb_status dobb_clip_grads(int num_tensors, const void* const* G, const int32_t
  *   mean, rstd  rows floats each (what the gradient needs)
  *   eps      a positive normal number
  * Outputs share no memory with each other or with what is read (refused), but
- * for out_dev in place of x_dev.  rows may be 0; dim is 1 ... 2^30 - 1. */
+ * for out_dev in place of x_dev.  rows may be 0; dim is 1 ... 2^30 - 1.
+ * The waits for copies are bounded as dobb_log_probs' are: a row that a wait gave up on
+ * has NaN for mean, rstd and out (there is no flag). */
 dobb_status dobb_layer_norm(const void* x_dev, dobb_dtype x_dtype, int64_t rows, int64_t dim,
                             int64_t x_stride, const void* weight_dev, const void* bias_dev,
                             dobb_dtype param_dtype, float eps, void* out_dev,
@@ -523,7 +525,8 @@ size_t dobb_layer_norm_backward_bytes(int64_t rows, int64_t dim);
  * stride); any other overlap of an output is refused.  workspace_dev is
  * caller memory of at least dobb_layer_norm_backward_bytes(), 256-byte aligned;
  * it holds nothing between calls.  With no rows dweight and dbias are zeros
- * (accumulate 0). */
+ * (accumulate 0).  A row that a wait for its copies gave up on has NaN for dx, and
+ * dweight and dbias are NaN. */
 dobb_status dobb_layer_norm_backward(const void* grad_dev, dobb_dtype grad_dtype,
                                      int64_t grad_stride, const void* x_dev, dobb_dtype x_dtype,
                                      int64_t rows, int64_t dim, int64_t x_stride,
@@ -540,6 +543,24 @@ dobb_status dobb_layer_norm_backward(const void* grad_dev, dobb_dtype grad_dtype
 int64_t dobb_selftest_layer_norm_smem(int64_t rows, int64_t dim, dobb_dtype x_dtype, int64_t x_stride,
                                       dobb_dtype grad_dtype, int64_t grad_stride, int backward,
                                       int64_t* most);
+
+/* Self-tests of the bounded waits of dobb_layer_norm and dobb_layer_norm_backward, with a
+ * limit of timeout_ns (1 ns ... 5 s): rows from loaded_rows on are not copied in (but for
+ * those that share a copy with an earlier one), so that the waits for them run out.
+ * DOBB_ERR_UNSUPPORTED for sizes that are computed without such waits. */
+dobb_status dobb_selftest_layer_norm_timeout(const void* x_dev, dobb_dtype x_dtype, int64_t rows,
+                                             int64_t dim, int64_t x_stride, const void* weight_dev,
+                                             const void* bias_dev, dobb_dtype param_dtype, float eps,
+                                             void* out_dev, dobb_dtype out_dtype, int64_t out_stride,
+                                             float* mean_dev, float* rstd_dev, void* stream,
+                                             int64_t loaded_rows, uint64_t timeout_ns);
+dobb_status dobb_selftest_layer_norm_backward_timeout(
+    const void* grad_dev, dobb_dtype grad_dtype, int64_t grad_stride, const void* x_dev,
+    dobb_dtype x_dtype, int64_t rows, int64_t dim, int64_t x_stride, const void* weight_dev,
+    dobb_dtype param_dtype, const float* mean_dev, const float* rstd_dev, void* dx_dev,
+    int64_t dx_stride, void* dweight_dev, void* dbias_dev, dobb_dtype dparam_dtype, int accumulate,
+    void* workspace_dev, size_t workspace_bytes, void* stream, int64_t loaded_rows,
+    uint64_t timeout_ns);
 
 /* Largest number of a teacher's entries per row. */
 #define DOBB_MAX_TEACHER 256
