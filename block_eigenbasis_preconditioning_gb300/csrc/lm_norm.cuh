@@ -207,11 +207,10 @@ template <typename T>
 __device__ __forceinline__ uint32_t copy_in(unsigned char* image, const T* p, int64_t n, const T* begin, const T* end, uint64_t* bar) {
   const uintptr_t from = reinterpret_cast<uintptr_t>(p), to = from + (uint64_t)n * sizeof(T);
   uintptr_t lo = from & ~(uintptr_t)15, hi = (to + 15) & ~(uintptr_t)15;
-  image -= lo & 15;
-  unsigned char* const base = image;
   const uintptr_t granule = lo;
   const auto by_value = [&](uintptr_t a, uintptr_t b) {
-    for (; a < b; a += sizeof(T)) *reinterpret_cast<T*>(base + (a - granule)) = *reinterpret_cast<const T*>(a);
+    for (; a < b; a += sizeof(T)) *reinterpret_cast<T*>(image + (a - granule)) = *reinterpret_cast<const T*>(a);
+    ptx::fence_proxy_async_smem();  // a later turn's copy comes over it
   };
   if (lo < reinterpret_cast<uintptr_t>(begin)) {
     lo += 16;
@@ -222,7 +221,7 @@ __device__ __forceinline__ uint32_t copy_in(unsigned char* image, const T* p, in
     by_value(hi > from ? hi : from, to);
   }
   if (hi <= lo) return 0;
-  ptx::bulk_load(base + (lo - granule), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
+  ptx::bulk_load(image + (lo - granule), reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo), bar);
   return (uint32_t)(hi - lo);
 }
 
