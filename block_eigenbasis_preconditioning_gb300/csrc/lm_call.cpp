@@ -73,14 +73,15 @@ struct Call {
   cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 };
 
-// f without the interpreter's lock
+// f without the interpreter's lock, which comes back where f throws, too (a tensor without
+// memory has no data pointer)
 template <typename F>
 bool launched(F f) {
-  dobb_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
-  return st == DOBB_OK;
+  struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  } unlocked;
+  return f() == DOBB_OK;
 }
 
 PyObject* tuple(std::initializer_list<Tensor> tensors) {
