@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 from typing import List, Optional, Sequence, Tuple
 
 from . import build as _build
@@ -140,7 +141,7 @@ def load_library(build_if_missing: bool = True):
     global _LIB
     if _LIB is not None:
         return _LIB
-    path = _build.build() if build_if_missing else _build.LIB
+    path = _build.build_library() if build_if_missing else _build.LIB
     if not os.path.exists(path):
         raise RuntimeError(f"libdobb.so not found at {path}; run build() first")
     lib = ctypes.CDLL(path)
@@ -152,14 +153,29 @@ def load_library(build_if_missing: bool = True):
     return lib
 
 
+class _NoCall:
+    """Stands for _lm_call.so where it cannot be compiled: it takes no call, so that lm.py's own way does."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def load_call():
-    """Load _lm_call.so (csrc/lm_call.cpp), which is built with the library."""
+    """Load _lm_call.so (csrc/lm_call.cpp), compiling it first if it is missing or stale."""
     global _CALL
     if _CALL is None:
         load_library()
-        spec = importlib.util.spec_from_file_location("_lm_call", _build.CALL)
-        _CALL = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_CALL)
+        try:
+            path = _build.build_call()
+        except _build.NoHeaders as e:
+            warnings.warn(f"calls of the language-model operators take about twice the host time, as _lm_call.so cannot be compiled: {e}",
+                          RuntimeWarning, stacklevel=3)
+            _CALL = _NoCall()
+            return _CALL
+        spec = importlib.util.spec_from_file_location("_lm_call", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _CALL = module
     return _CALL
 
 
