@@ -26,7 +26,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
-from operator import attrgetter
+from operator import attrgetter, index as whole_index
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -189,6 +189,22 @@ def _flags(flags: Optional[torch.Tensor]) -> Optional[int]:
     return flags.data_ptr()
 
 
+def _number(v, name: str) -> float:
+    try:
+        if not isinstance(v, str):
+            return float(v)
+    except (TypeError, ValueError):
+        pass
+    raise ValueError(f"{name} must be a number, got {v!r}")
+
+
+def _whole(v, name: str) -> int:
+    try:
+        return whole_index(v)
+    except TypeError as e:
+        raise ValueError(f"{name} must be a whole number, got {v!r}") from e
+
+
 def _float_dtype(dtype: torch.dtype, name: str) -> int:
     code = _DTYPES.get(dtype)
     if code is None:
@@ -314,6 +330,7 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *, s
         r = load_call().distill(logits, ids, teacher, scale, teacher_scale, grad_loss)
         if r is not None:
             return Distilled(*r, float(scale), float(teacher_scale))
+    scale, teacher_scale = _number(scale, "scale"), _number(teacher_scale, "teacher_scale")
     stride = _rows(logits, "logits")
     dtype = _float_dtype(logits.dtype, "logits")
     rows, vocab = logits.shape
@@ -366,7 +383,7 @@ def distill_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
 def _setting(v, rows: int, dtype: torch.dtype, name: str):
     """(the one value, pointer to one per row) of a setting."""
     if not isinstance(v, torch.Tensor):
-        return v, None
+        return (_whole if dtype is torch.int32 else _number)(v, name), None
     if v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
         raise ValueError(f"{name} must be a number or {rows} contiguous {dtype} values")
     return 1, v.data_ptr()
@@ -444,6 +461,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         r = load_call().layer_norm(x, weight, bias, eps, out_dtype)
         if r is not None:
             return LayerNorm(*r)
+    eps = _number(eps, "eps")
     m = x if x.dim() == 2 else _as_rows(x, "x")
     stride = _rows(m, "x")
     xdtype = _float_dtype(x.dtype, "x")
