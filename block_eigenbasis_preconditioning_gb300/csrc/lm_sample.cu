@@ -1473,9 +1473,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
       Part listed;
       listed.at = -1;
       general = false;
-      if (ranked) {
-        const int n = sh.nlist;
-        // the border lies in the list, or the list goes to the row's end
+      if (top_p < 1.f) {
+        // what is kept so far lies below top_p's share, so none of it is too much: the bins are
+        // as exact as fp32 is at the maximum, and min-p may have ended in a gap at the border
         Pair rest;
         const Pair all = total();
         const float share = top_p * all.hi;
@@ -1484,8 +1484,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_rows(const SampleArgs a) {
         rest.add(fmaf(top_p, all.hi, -share));
         rest.add(fmaf(top_p, all.lo, -kept.lo));
         const unsigned long long want = whole_mass(rest);
+        const int n = sh.nlist;
         general = n > kList || want == 0;
-        if (!general) {
+        if (ranked && !general) {
+          // the border lies in the list, or the list goes to the row's end
           unsigned long long cut = 0;
           if (list_mass(sh, n, 0, r) >= want)
             cut = list_border(sh, n, 0, want, r, list_x, fminf(above_x, m), a.vocab);

@@ -74,3 +74,32 @@ def test_top_p_over_half_a_million_nearly_equal_masses():
     kept = rank[which, r.tokens.cpu().numpy()]
     off = np.maximum(upto[which, kept - 1] - share, share - upto[which, kept]) / slack[which]
     assert (off <= 1).all(), f"{int((off > 1).sum())} of {rows} rows end {off.max():.1f} times too far from the border ({kept[off.argmax()] - last[off.argmax()]} entries)"
+
+
+@pytest.mark.parametrize("offset", [40000.0, -37000.0, 700.0])
+def test_min_p_that_ends_right_behind_top_p(offset):
+    """Logits far from 0, so that what top_p's bins are relative to is coarse in fp32 (2^-9 of a power of two), and
+    a gap below the border: min_p ends in the gap, top_p a few entries before it."""
+    import block_eigenbasis_preconditioning_gb300 as d
+    rows, vocab, upper, around = 256, 40000, 20000, 40
+    rng = np.random.default_rng(24)
+    x = np.empty((rows, vocab), dtype=np.float32)
+    x[:, :upper] = offset + rng.uniform(-0.2, 0, size=(rows, upper))
+    x[:, upper:] = offset + rng.uniform(-3.2, -3, size=(rows, vocab - upper))
+    order = np.argsort(-x, axis=1, kind="stable")
+    s = np.take_along_axis(x, order, 1).astype(np.float64)
+    p = np.exp(s - s[:, :1])
+    upto = p.cumsum(1)
+    top_p = np.float32(upto[:, upper - 1] / upto[:, -1] - np.linspace(2e-5, 1.5e-3, rows))
+    share = top_p.astype(np.float64) * upto[:, -1]
+    last = (upto < share[:, None]).sum(1)  # the entry that crosses the border is kept
+    noise = torch.ones(rows, vocab, device="cuda")
+    at = np.stack([order[i, upper - 2 * around:upper] for i in range(rows)])
+    noise.scatter_(1, torch.from_numpy(at).cuda(), torch.logspace(-2, -36, 2 * around, device="cuda").expand(rows, -1))
+    r = d.sample(torch.from_numpy(x).cuda(), noise, top_p=torch.from_numpy(top_p).cuda(), min_p=float(np.exp(-1.5)))
+    kept = np.array([int(np.where(order[i] == int(t))[0][0]) for i, t in enumerate(r.tokens.cpu())])
+    w = (p * -np.log(p)).sum(1) / upto[:, -1]
+    slack = (3 * w + 32) * 2.0 ** -24 * upto[:, -1]
+    i = np.arange(rows)
+    off = np.maximum(np.where(kept > 0, upto[i, kept - 1], 0.0) - share, share - upto[i, kept]) / slack
+    assert (off <= 1).all(), f"{int((off > 1).sum())} of {rows} rows, up to {(kept - last)[off.argmax()]} entries off"
