@@ -82,6 +82,8 @@ def _call_includes():
         import torch
     except ImportError as e:
         raise NoHeaders(f"PyTorch is not installed ({e})") from e
+    if not torch.version.cuda:
+        raise NoHeaders("PyTorch was built without CUDA")
     base = os.path.join(os.path.dirname(torch.__file__), "include")
     python = sysconfig.get_paths()["include"]
     for f in (os.path.join(python, "Python.h"), os.path.join(base, "ATen", "core", "Tensor.h")):

@@ -102,3 +102,8 @@ def test_a_compiler_that_fails_is_an_error(folder, monkeypatch):
     with pytest.raises(RuntimeError, match="lm_call"):
         build.build()
     assert os.path.exists(build.LIB)  # (the library is there)
+
+
+def test_a_pytorch_without_cuda(folder, monkeypatch, capsys):
+    monkeypatch.setattr(torch.version, "cuda", None)
+    assert build.build() == build.LIB and not set(folder) & set(CALL) and "without CUDA" in capsys.readouterr().out
