@@ -177,6 +177,12 @@ __device__ __forceinline__ float log_p(float x, float m, float log_sum, float sc
   return scaled_difference(x, m, scale) - log_sum;
 }
 
+// The share in the loss of a logit at the end of fp32, whose log p lies beyond.  (A call, as inline it costs the
+// loss and gradient of 8192 x 50257 bf16 half a percent more.)
+__device__ __noinline__ float far_share(float q, float log_q, float x, float m, float log_sum, float scale) {
+  return (float)((double)q * ((double)log_q - ((double)scale * ((double)x - (double)m) - (double)log_sum)));
+}
+
 // The loss of a row by one warp; the teacher's entries are in t, x_at(i) is
 // the student's logit of entry i.
 template <typename F>
@@ -185,7 +191,12 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, const Teacher& 
   float s = 0.f;
   for (int i = lane; i < a.k; i += 32) {
     const float q = t.q[i];
-    if (t.id[i] >= 0 && q != 0.f) s = fmaf(q, t.log_q[i] - log_p(x_at(i), m, log_sum, a.scale), s);
+    if (t.id[i] < 0 || q == 0.f) continue;
+    const float x = x_at(i), lp = log_p(x, m, log_sum, a.scale);
+    if (lp == -INFINITY && x != -INFINITY)
+      s += far_share(q, t.log_q[i], x, m, log_sum, a.scale);
+    else
+      s = fmaf(q, t.log_q[i] - lp, s);
   }
   s = warp_sum(s);
   if (lane == 0) {

@@ -579,7 +579,8 @@ dobb_status dobb_selftest_layer_norm_backward_timeout(
  * entries: 0).
  * With grad_loss (g, rows floats) and dlogits also the gradient of sum_r g loss:
  *   dlogits[r][j] = scale * g (p_j - sum_{i: ids[r][i] = j} q_i)
- * zeros in rows without entries, with an id >= vocab or with logits of -inf alone.
+ * zeros in rows without entries, with an id >= vocab or with logits of -inf alone.  A
+ * p_j below 2^-126 counts as 0.
  *   logits_dev  rows x vocab, row r at r * row_stride elements
  *   ids_dev     rows x k, int32 or int64 (id_bytes 4 or 8); teacher_dev rows x k
  *   k           1 ... DOBB_MAX_TEACHER
