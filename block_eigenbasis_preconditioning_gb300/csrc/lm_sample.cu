@@ -14,11 +14,11 @@
 // cluster's of one to eight blocks.
 //
 // Measured (in a graph): 512 x 128256 bf16 unfiltered 74 us (78 % of the copy rate),
-// min_p 0.05 68, top_k 50 42; 509 x 50257 bf16 39, 32 and 25, top_p 0.9 91 (issue slots:
-// 70 instructions an entry for the sum, the bins and the choice, 4700 kept of a row);
+// min_p 0.05 68, top_k 50 42; 509 x 50257 bf16 39, 32 and 25, top_p 0.9 93 (issue slots:
+// 71 instructions an entry for the sum, the bins and the choice, 4700 kept of a row);
 // one row of 50257 with top_k 50 and top_p 0.95 11 (a chain of eight cluster
 // barriers and shared-memory rounds).  A top_k above 1024 goes the general way:
-// 509 x 50257 with top_k 2000 317 us.
+// 509 x 50257 with top_k 2000 322 us.
 //
 // The token is the kept one with the largest y - log E, E ~ Exp(1): token j with
 // probability e^{y_j} / sum over the kept.  The entries within a margin of the
